@@ -396,6 +396,121 @@ MATE_API mate_status mate_dit_block_forward(const void* X, const float* c, int d
                                             void* ws, size_t ws_bytes, mate_stream_t stream);
 
 /*
+ * Norms of queries and keys for each head, with the rotation by the token's position in the same pass: an
+ * optional step between the qkv projection and tesa_forward, on the same packed rows (the pages describe
+ * neither; both are common companions of such an attention).  Rows are grid tokens, row b*T*H*W + (t*H + h)*W + w
+ * (a plain sequence of length L: T = L, H = W = 1); a row holds hq query heads, hk key heads and hv value heads
+ * of tp channels each (tesa_forward: hq = hk = hv = th).  Per query or key head vector x[tp]:
+ *     y = x / sqrt(mean(x^2) + eps) * w             (w = wq or wk [tp], shared by the heads; null: 1)
+ *     channels [0, rt) turn by the t tables, [rt, rt + rh) by h, [rt + rh, rt + rh + rw) by w, the rest stay:
+ *     pair (u, v) of an axis' channels -> (u cos - v sin, v cos + u sin) with entry i of the token's table row;
+ *     pairing 0: pair i = channels 2i, 2i + 1 of the axis' block; pairing 1: channels i, i + r/2.
+ * Tables: [T][rt/2], [H][rh/2], [W][rw/2] pairs (cos, sin) of floats, as mate_rope_table writes them (any table
+ * of that layout serves; a later part of a video passes tables that start at its first frame).
+ * Requirements: rt, rh, rw even, rt + rh + rw <= tp, tp <= 256, tp a multiple of 16 bytes of elements, hq and
+ * hk at least 1, eps > 0, B*T*H*W < 2^31.  fp32 arithmetic, one rounding at the end.
+ */
+typedef struct {
+  int B, T, H, W;
+  int hq, hk, hv, tp;
+  int rt, rh, rw;
+  int pairing;      /* 0: adjacent channels, 1: halves of the axis' block */
+  float eps;
+  mate_dtype dtype;
+} mate_qk_config;
+
+/* table[p][i] = (cos, sin) of (start + p) theta^(-2i/dims), p < count, i < dims/2; the angle in double. */
+MATE_API mate_status mate_rope_table(float* table, long long start, int count, int dims, double theta,
+                                     mate_stream_t stream);
+
+/*
+ * qkv rows -> out rows (row strides ldi, ldo in elements: at least (hq + hk + hv)*tp and a multiple of 16 bytes).
+ * out == qkv (ldo == ldi) works in place: the value columns stay as they are; otherwise they are copied, and the
+ * two must not overlap.  Tables of an axis with 0 channels may be null.
+ */
+MATE_API mate_status mate_qk_norm_rope(const void* qkv, long long ldi, const float* wq, const float* wk,
+                                       const float* tab_t, const float* tab_h, const float* tab_w, void* out,
+                                       long long ldo, const mate_qk_config* cfg, mate_stream_t stream);
+
+/*
+ * Backward pass of mate_qk_norm_rope: from its input qkv and the output gradient dout (same columns) the input
+ * gradient dqkv (query and key columns by the chain rule, value columns copied) and the weight gradients dwq, dwk
+ * [tp] (each may be null), summed over rows and heads in a fixed order.  dqkv may be dout or qkv itself (same
+ * row stride).  ws: at least mate_qk_norm_rope_backward_workspace_bytes(cfg) bytes.
+ */
+MATE_API size_t mate_qk_norm_rope_backward_workspace_bytes(const mate_qk_config* cfg);
+MATE_API mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, const float* wq, const float* wk,
+                                                const float* tab_t, const float* tab_h, const float* tab_w,
+                                                const void* dout, long long ldg, void* dqkv, long long ldd, float* dwq,
+                                                float* dwk, const mate_qk_config* cfg, void* ws, size_t ws_bytes,
+                                                mate_stream_t stream);
+
+/*
+ * Gated linear recurrence over the tokens of a grid, a companion of ssd_scan_bidir with an elementwise state (the
+ * pages describe only the selective scan).  Per sample and channel, along scan order `order` (0..3, as rms_permute;
+ * the rows stay in grid order) from its first position to its last (reverse = 1: from the last to the first):
+ *     a_t = sigmoid(g_t + bias),   h_t = a_t h_{t-1} + (1 - a_t) x_t,   y_t = h_t
+ * Both directions are two calls, and a video in parts or token by token hands h_last to the next call as h0.
+ *   x, g, y   rows b*T*H*W + (t*H + h)*W + w of D channels, row strides ldx, ldg, ldy in elements (at least D and a
+ *             multiple of 16 bytes); y must not overlap x or g
+ *   bias [D] (null: 0), h0 [B, D] state before the first row (null: 0), h_last [B, D] state after the last row
+ *             (null: not wanted), all float
+ *   states    (null: not wanted) for the backward pass: mate_gated_scan_states_bytes(cfg) bytes, overwritten with
+ *             the state before each run of rows
+ * Requirements: D a multiple of 16 bytes of elements, B*T*H*W < 2^31.  ws: at least
+ * mate_gated_scan_workspace_bytes(cfg) bytes; calls that overlap on the GPU need workspaces of their own.
+ * States and gates are fp32; the result does not change from run to run.
+ */
+typedef struct {
+  int B, T, H, W, D;
+  int order;        /* 0..3 */
+  int reverse;      /* 0 or 1 */
+  mate_dtype dtype;
+} mate_gated_scan_config;
+
+MATE_API size_t mate_gated_scan_workspace_bytes(const mate_gated_scan_config* cfg);
+MATE_API size_t mate_gated_scan_states_bytes(const mate_gated_scan_config* cfg);
+MATE_API mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long long ldg, const float* bias,
+                                     const float* h0, void* y, long long ldy, float* h_last, float* states,
+                                     const mate_gated_scan_config* cfg, void* ws, size_t ws_bytes,
+                                     mate_stream_t stream);
+
+/*
+ * Backward pass of mate_gated_scan from its inputs, the `states` it wrote (same cfg; they hold h0), the gradient dy
+ * of y and the gradient dh_last [B, D] of h_last (null: 0):
+ *     l_t = dy_t + a_{t+1} l_{t+1},   dx_t = (1 - a_t) l_t,   dg_t = l_t (h_{t-1} - x_t) a_t (1 - a_t)
+ * dbias [D] = sum of dg over samples and rows (null: not wanted), dh0 [B, D] = a_1 l_1 (null: not wanted), both
+ * float, reproducible.  dx and dg must not overlap each other or an input.  ws: at least
+ * mate_gated_scan_backward_workspace_bytes(cfg) bytes.
+ */
+MATE_API size_t mate_gated_scan_backward_workspace_bytes(const mate_gated_scan_config* cfg);
+MATE_API mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g, long long ldg,
+                                              const float* bias, const float* states, const void* dy, long long lddy,
+                                              const float* dh_last, void* dx, long long lddx, void* dg, long long lddg,
+                                              float* dbias, float* dh0, const mate_gated_scan_config* cfg, void* ws,
+                                              size_t ws_bytes, mate_stream_t stream);
+
+/*
+ * Projection in 8-bit integers beside mate_project_bf16 (inference; no counterpart in the pages): activations are
+ * quantised row by row as they come, weights once, with one scale per token and per output channel.
+ *
+ * mate_quantize_rows: x [M, K] of type `dtype` (row stride ldx, rows on 16 bytes) -> q [M, K] int8 (row stride ldq,
+ * a multiple of 16) and scale [M]:  scale = max|x| / 127 in fp32,  q = x / scale to the nearest integer, ties to
+ * even, decided exactly.  A row of zeros gets scale 0 and q = 0; a row with an infinity or a NaN gets scale NaN and
+ * q = 0 (its projection is NaN).
+ *
+ * mate_project_int8: C[m, n] = (sum_k A[m, k] W[n, k]) a_scale[m] w_scale[n] + bias[n], the sum exact in 32 bits,
+ * the rest in fp32, rounded once to out_dtype.  A [M, K] and Wt [N, K] int8 (row strides lda, ldw, multiples of 16,
+ * any K < 131072), a_scale [M], w_scale [N], bias [N] (null: none) float, C [M, N] (row stride ldc >= N elements).
+ * M = 0 does nothing.
+ */
+MATE_API mate_status mate_quantize_rows(const void* x, long long ldx, long long M, int K, mate_dtype dtype, void* q,
+                                        long long ldq, float* scale, mate_stream_t stream);
+MATE_API mate_status mate_project_int8(const void* A, long long lda, const float* a_scale, long long M, int K,
+                                       const void* Wt, long long ldw, const float* w_scale, int N, const float* bias,
+                                       void* C, long long ldc, mate_dtype out_dtype, mate_stream_t stream);
+
+/*
  * Reads and clears the device status word that kernels set when a bounded wait runs out.  Synchronises
  * `stream` first, then takes the word with one atomic exchange on the device (a flag that a kernel on
  * another stream sets meanwhile is reported now or by the next call, never dropped), and synchronises
@@ -444,7 +559,16 @@ typedef enum {
   MATE_K_MLP_UP = 23,          /* DiT block: gelu(h W1^T + b1) */
   MATE_K_MLP_DOWN = 24,        /* DiT block: X1 + gate_m (Z W2^T + b2) */
   MATE_K_TESA_BWD_DQ = 25,     /* tesa_backward: row statistics, delta and dQ */
-  MATE_K_TESA_BWD_DKDV = 26    /* tesa_backward: dK and dV */
+  MATE_K_TESA_BWD_DKDV = 26,   /* tesa_backward: dK and dV */
+  MATE_K_ROPE_TABLE = 27,      /* mate_rope_table */
+  MATE_K_QK_NORM_ROPE = 28,    /* mate_qk_norm_rope */
+  MATE_K_QK_NORM_ROPE_BWD = 29, /* mate_qk_norm_rope_backward: dqkv and partial weight gradients */
+  MATE_K_QK_WEIGHT_GRAD = 30,  /* mate_qk_norm_rope_backward: sum of the partial weight gradients */
+  MATE_K_GATED_SCAN = 31,      /* mate_gated_scan */
+  MATE_K_GATED_SCAN_BWD = 32,  /* mate_gated_scan_backward */
+  MATE_K_QUANTIZE_ROWS = 33,   /* mate_quantize_rows */
+  MATE_K_PROJECT_INT8 = 34,    /* mate_project_int8 */
+  MATE_K_GATED_SCAN_BIAS = 35  /* mate_gated_scan_backward: sum of the partial bias gradients */
 } mate_kernel;
 
 typedef struct {

@@ -20,6 +20,10 @@ EXPORTS = (
     "mate_ssd_backward_workspace_bytes", "mate_selftest_wait_timeout", "mate_forward_host_pipelined",
     "mate_packed_weights_bytes", "mate_pack_weights", "mate_dit_workspace_bytes", "mate_dit_block_forward",
     "mate_forward_host_flush", "mate_tesa_backward_workspace_bytes", "tesa_backward",
+    "mate_rope_table", "mate_qk_norm_rope", "mate_qk_norm_rope_backward",
+    "mate_qk_norm_rope_backward_workspace_bytes", "mate_gated_scan", "mate_gated_scan_workspace_bytes",
+    "mate_gated_scan_states_bytes", "mate_gated_scan_backward", "mate_gated_scan_backward_workspace_bytes",
+    "mate_quantize_rows", "mate_project_int8",
 )
 
 _CONFIG_FIELDS = ("B", "T", "H", "W", "d", "nh", "P", "N", "Q", "R", "th", "tp", "wt", "wh", "ww", "st", "sh", "sw")
@@ -27,6 +31,15 @@ _CONFIG_FIELDS = ("B", "T", "H", "W", "d", "nh", "P", "N", "Q", "R", "th", "tp",
 
 class CConfig(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int) for f in _CONFIG_FIELDS] + [("dtype", ctypes.c_int), ("mamba_extras", ctypes.c_int)]
+
+
+class CQkConfig(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("B", "T", "H", "W", "hq", "hk", "hv", "tp", "rt", "rh", "rw", "pairing")] + \
+        [("eps", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+class CGatedScanConfig(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_int) for f in ("B", "T", "H", "W", "D", "order", "reverse", "dtype")]
 
 
 class CWeights(ctypes.Structure):
@@ -63,7 +76,8 @@ def load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libmate.so is not built ({LIB_PATH}); run linear_complexity_video_mate_b200.build")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, ci, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    vp, ci, sz, ll = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_longlong
+    qkp, gsp = ctypes.POINTER(CQkConfig), ctypes.POINTER(CGatedScanConfig)
     cfgp, wp = ctypes.POINTER(CConfig), ctypes.POINTER(CWeights)
     sigs = {
         "mate_status_str": (ctypes.c_char_p, [ci]),
@@ -99,6 +113,17 @@ def load():
         "mate_forward_host_workspace_bytes": (sz, [cfgp]),
         "mate_device_status": (ci, [vp, ctypes.POINTER(ctypes.c_uint)]),
         "mate_last_launch_count": (ci, []),
+        "mate_rope_table": (ci, [vp, ll, ci, ci, ctypes.c_double, vp]),
+        "mate_qk_norm_rope": (ci, [vp, ll] + [vp] * 6 + [ll, qkp, vp]),
+        "mate_qk_norm_rope_backward_workspace_bytes": (sz, [qkp]),
+        "mate_qk_norm_rope_backward": (ci, [vp, ll] + [vp] * 6 + [ll, vp, ll, vp, vp, qkp, vp, sz, vp]),
+        "mate_gated_scan_workspace_bytes": (sz, [gsp]),
+        "mate_gated_scan_states_bytes": (sz, [gsp]),
+        "mate_gated_scan_backward_workspace_bytes": (sz, [gsp]),
+        "mate_gated_scan": (ci, [vp, ll, vp, ll, vp, vp, vp, ll, vp, vp, gsp, vp, sz, vp]),
+        "mate_gated_scan_backward": (ci, [vp, ll, vp, ll, vp, vp, vp, ll, vp, vp, ll, vp, ll, vp, vp, gsp, vp, sz, vp]),
+        "mate_quantize_rows": (ci, [vp, ll, ll, ci, ci, vp, ll, vp, vp]),
+        "mate_project_int8": (ci, [vp, ll, vp, ll, ci, vp, ll, vp, ci, vp, vp, ll, ci, vp]),
         "mate_project_bf16": (ci, [vp, ci, ctypes.c_longlong, ci, vp, ci, ci, vp, ci, vp]),
     }
     for name, (res, args) in sigs.items():

@@ -23,6 +23,9 @@
 #include "ssd_backward.cuh"
 #include "dit.cuh"
 #include "tesa_backward.cuh"
+#include "qk_norm_rope.cuh"
+#include "gated_scan.cuh"
+#include "gemm_int8.cuh"
 
 using namespace mate;
 
@@ -1538,8 +1541,19 @@ const char* mate_kernel_name(int kernel) {
     case MATE_K_MLP_DOWN: return "mlp_down";
     case MATE_K_TESA_BWD_DQ: return "tesa_backward_dq";
     case MATE_K_TESA_BWD_DKDV: return "tesa_backward_dkdv";
+    case MATE_K_ROPE_TABLE: return "rope_table";
+    case MATE_K_QK_NORM_ROPE: return "qk_norm_rope";
+    case MATE_K_QK_NORM_ROPE_BWD: return "qk_norm_rope_backward";
+    case MATE_K_QK_WEIGHT_GRAD: return "qk_weight_grad";
+    case MATE_K_GATED_SCAN: return "gated_scan";
+    case MATE_K_GATED_SCAN_BWD: return "gated_scan_backward";
+    case MATE_K_GATED_SCAN_BIAS: return "gated_scan_bias";
+    case MATE_K_QUANTIZE_ROWS: return "quantize_rows";
+    case MATE_K_PROJECT_INT8: return "project_int8";
   }
   return "unknown";
 }
 
 }  // extern "C"
+
+#include "operators_api.cuh"

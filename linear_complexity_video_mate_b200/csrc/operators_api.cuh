@@ -1,0 +1,364 @@
+// Host side of the operators beside the block: q/k norm with rotation, gated scan, 8-bit projection.  Included by mate_api.cu (it uses that
+// file's validation, trace and launch helpers).
+#pragma once
+
+namespace {
+
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// ------------------------------------------------------------------------------ q/k norm with rotation
+mate_status check_qk(const mate_qk_config* c) {
+  if (c == nullptr) return MATE_ERR_ARG;
+  if (c->dtype != MATE_BF16 && c->dtype != MATE_F32) return MATE_ERR_ARG;
+  if (c->pairing != 0 && c->pairing != 1) return MATE_ERR_ARG;
+  if (!(c->eps > 0.f) || !std::isfinite(c->eps)) return MATE_ERR_ARG;
+  if (c->B <= 0 || c->T <= 0 || c->H <= 0 || c->W <= 0 || c->hq <= 0 || c->hk <= 0 || c->hv < 0 || c->tp <= 0 ||
+      c->rt < 0 || c->rh < 0 || c->rw < 0)
+    return MATE_ERR_SHAPE;
+  if (c->rt % 2 || c->rh % 2 || c->rw % 2 || (long long)c->rt + c->rh + c->rw > c->tp) return MATE_ERR_SHAPE;
+  const int es = c->dtype == MATE_BF16 ? 2 : 4;
+  if (c->tp > kQkMaxDim) return MATE_ERR_UNSUPPORTED;
+  if (c->tp * es % 16) return MATE_ERR_SHAPE;
+  if (((long long)c->hq + c->hk + c->hv) * c->tp >= (1LL << 31)) return MATE_ERR_SHAPE;
+  // 64-bit products of three factors below 2^31 fit; a fourth is checked by division
+  const long long hw = (long long)c->H * c->W;
+  if (hw >= (1LL << 31) || hw * c->T >= (1LL << 31) || hw * c->T * c->B >= (1LL << 31)) return MATE_ERR_SHAPE;
+  return MATE_OK;
+}
+
+// Row stride in elements: rows start on 16 bytes and hold `width` elements.
+bool row_stride_ok(long long ld, long long width, int es) { return ld >= width && ld * es % 16 == 0; }
+
+mate_status fill_qk(const mate_qk_config* c, const void* x, long long ldx, const float* wq, const float* wk,
+                    const float* tt, const float* th, const float* tw, QkParams* p) {
+  const long long width = ((long long)c->hq + c->hk + c->hv) * c->tp;
+  const int es = c->dtype == MATE_BF16 ? 2 : 4;
+  if (x == nullptr || !aligned16(x) || !aligned16(wq) || !aligned16(wk) || !row_stride_ok(ldx, width, es))
+    return MATE_ERR_ARG;
+  if ((c->rt > 0 && tt == nullptr) || (c->rh > 0 && th == nullptr) || (c->rw > 0 && tw == nullptr) || !aligned8(tt) ||
+      !aligned8(th) || !aligned8(tw))
+    return MATE_ERR_ARG;
+  p->x = x;
+  p->ldx = ldx;
+  p->wq = wq;
+  p->wk = wk;
+  p->tab_t = reinterpret_cast<const float2*>(tt);
+  p->tab_h = reinterpret_cast<const float2*>(th);
+  p->tab_w = reinterpret_cast<const float2*>(tw);
+  p->rows = (long long)c->B * c->T * c->H * c->W;
+  p->T = c->T;
+  p->H = c->H;
+  p->W = c->W;
+  p->hq = c->hq;
+  p->hk = c->hk;
+  p->hv = c->hv;
+  p->tp = c->tp;
+  p->rt = c->rt;
+  p->rh = c->rh;
+  p->rw = c->rw;
+  p->pairing = c->pairing;
+  p->eps = c->eps;
+  return MATE_OK;
+}
+
+int qk_blocks(const QkParams& p) {
+  return static_cast<int>(std::min<long long>((p.rows + kQkWarps - 1) / kQkWarps,
+                                              std::min(kQkMaxBlocks, 8 * device_sms())));
+}
+
+}  // namespace
+
+extern "C" {
+
+mate_status mate_rope_table(float* table, long long start, int count, int dims, double theta, mate_stream_t stream) {
+  if (table == nullptr || !aligned8(table) || !(theta > 0.0) || !std::isfinite(theta)) return MATE_ERR_ARG;
+  if (count <= 0 || dims <= 0 || dims % 2) return MATE_ERR_SHAPE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  t_launches = 0;
+  const long long total = (long long)count * (dims / 2);
+  trace_begin(MATE_K_ROPE_TABLE, st);
+  rope_table_kernel<<<static_cast<int>(std::min<long long>((total + 255) / 256, 4096)), 256, 0, st>>>(
+      reinterpret_cast<float2*>(table), static_cast<double>(start), count, dims / 2, theta);
+  MATE_LAUNCH_CHECK();
+  return MATE_OK;
+}
+
+mate_status mate_qk_norm_rope(const void* qkv, long long ldi, const float* wq, const float* wk, const float* tab_t,
+                              const float* tab_h, const float* tab_w, void* out, long long ldo,
+                              const mate_qk_config* cfg, mate_stream_t stream) {
+  MATE_TRY(check_qk(cfg));
+  QkParams p{};
+  MATE_TRY(fill_qk(cfg, qkv, ldi, wq, wk, tab_t, tab_h, tab_w, &p));
+  const int es = cfg->dtype == MATE_BF16 ? 2 : 4;
+  if (out == nullptr || !aligned16(out) ||
+      !row_stride_ok(ldo, ((long long)cfg->hq + cfg->hk + cfg->hv) * cfg->tp, es) || (out == qkv && ldo != ldi))
+    return MATE_ERR_ARG;
+  p.out = out;
+  p.ldo = ldo;
+  p.copy_v = cfg->hv > 0 && out != qkv;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  t_launches = 0;
+  trace_begin(MATE_K_QK_NORM_ROPE, st);
+  if (cfg->dtype == MATE_BF16) qk_norm_rope_kernel<__nv_bfloat16><<<qk_blocks(p), kQkWarps * 32, 0, st>>>(p);
+  else qk_norm_rope_kernel<float><<<qk_blocks(p), kQkWarps * 32, 0, st>>>(p);
+  MATE_LAUNCH_CHECK();
+  return MATE_OK;
+}
+
+size_t mate_qk_norm_rope_backward_workspace_bytes(const mate_qk_config* cfg) {
+  if (check_qk(cfg) != MATE_OK) return 0;
+  return (size_t)kQkMaxBlocks * 2 * cfg->tp * sizeof(float);
+}
+
+mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, const float* wq, const float* wk,
+                                       const float* tab_t, const float* tab_h, const float* tab_w, const void* dout,
+                                       long long ldg, void* dqkv, long long ldd, float* dwq, float* dwk,
+                                       const mate_qk_config* cfg, void* ws, size_t ws_bytes, mate_stream_t stream) {
+  MATE_TRY(check_qk(cfg));
+  QkParams p{};
+  MATE_TRY(fill_qk(cfg, qkv, ldi, wq, wk, tab_t, tab_h, tab_w, &p));
+  const int es = cfg->dtype == MATE_BF16 ? 2 : 4;
+  const long long width = ((long long)cfg->hq + cfg->hk + cfg->hv) * cfg->tp;
+  if (dout == nullptr || dqkv == nullptr || ws == nullptr || !aligned16(dout) || !aligned16(dqkv) || !aligned16(ws) ||
+      !row_stride_ok(ldg, width, es) || !row_stride_ok(ldd, width, es) || (dqkv == dout && ldd != ldg) ||
+      (dqkv == qkv && ldd != ldi))
+    return MATE_ERR_ARG;
+  if (ws_bytes < mate_qk_norm_rope_backward_workspace_bytes(cfg)) return MATE_ERR_WORKSPACE;
+  p.out = dqkv;
+  p.ldo = ldd;
+  p.dz = dout;
+  p.ldz = ldg;
+  p.part = static_cast<float*>(ws);
+  p.copy_v = cfg->hv > 0 && dqkv != dout;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  t_launches = 0;
+  const int blocks = qk_blocks(p);
+  trace_begin(MATE_K_QK_NORM_ROPE_BWD, st);
+  if (cfg->dtype == MATE_BF16) qk_norm_rope_bwd_kernel<__nv_bfloat16><<<blocks, kQkWarps * 32, 0, st>>>(p);
+  else qk_norm_rope_bwd_kernel<float><<<blocks, kQkWarps * 32, 0, st>>>(p);
+  MATE_LAUNCH_CHECK();
+  if (dwq != nullptr || dwk != nullptr) {
+    trace_begin(MATE_K_QK_WEIGHT_GRAD, st);
+    qk_weight_grad_kernel<<<ceil_div(2 * cfg->tp, 8), 256, 0, st>>>(p.part, blocks, cfg->tp, dwq, dwk);
+    MATE_LAUNCH_CHECK();
+  }
+  return MATE_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------ gated scan
+namespace {
+
+mate_status check_gated(const mate_gated_scan_config* c) {
+  if (c == nullptr) return MATE_ERR_ARG;
+  if (c->dtype != MATE_BF16 && c->dtype != MATE_F32) return MATE_ERR_ARG;
+  if (c->order < 0 || c->order > 3 || (c->reverse != 0 && c->reverse != 1)) return MATE_ERR_ARG;
+  if (c->B <= 0 || c->T <= 0 || c->H <= 0 || c->W <= 0 || c->D <= 0) return MATE_ERR_SHAPE;
+  if (c->D % (c->dtype == MATE_BF16 ? 8 : 4)) return MATE_ERR_SHAPE;
+  const long long hw = (long long)c->H * c->W;
+  if (hw >= (1LL << 31) || hw * c->T >= (1LL << 31) || hw * c->T * c->B >= (1LL << 31)) return MATE_ERR_SHAPE;
+  return MATE_OK;
+}
+
+mate_status fill_gated(const mate_gated_scan_config* c, const void* x, long long ldx, const void* g, long long ldg,
+                       const float* bias, GatedScanParams* p) {
+  const int es = c->dtype == MATE_BF16 ? 2 : 4;
+  if (x == nullptr || g == nullptr || !aligned16(x) || !aligned16(g) || !aligned16(bias) ||
+      !row_stride_ok(ldx, c->D, es) || !row_stride_ok(ldg, c->D, es))
+    return MATE_ERR_ARG;
+  p->x = x;
+  p->g = g;
+  p->ldx = ldx;
+  p->ldg = ldg;
+  p->bias = bias;
+  p->B = c->B;
+  p->T = c->T;
+  p->H = c->H;
+  p->W = c->W;
+  p->D = c->D;
+  p->order = c->order;
+  p->reverse = c->reverse;
+  return MATE_OK;
+}
+
+int gated_chunks(const mate_gated_scan_config* c) { return ceil_div((long long)c->T * c->H * c->W, kGsChunk); }
+
+}  // namespace
+
+extern "C" {
+
+size_t mate_gated_scan_workspace_bytes(const mate_gated_scan_config* cfg) {
+  if (check_gated(cfg) != MATE_OK) return 0;
+  return 256;
+}
+
+size_t mate_gated_scan_states_bytes(const mate_gated_scan_config* cfg) {
+  if (check_gated(cfg) != MATE_OK) return 0;
+  return (size_t)cfg->B * gated_chunks(cfg) * cfg->D * sizeof(float);
+}
+
+mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long long ldg, const float* bias,
+                            const float* h0, void* y, long long ldy, float* h_last, float* states,
+                            const mate_gated_scan_config* cfg, void* ws, size_t ws_bytes, mate_stream_t stream) {
+  MATE_TRY(check_gated(cfg));
+  GatedScanParams p{};
+  MATE_TRY(fill_gated(cfg, x, ldx, g, ldg, bias, &p));
+  const int es = cfg->dtype == MATE_BF16 ? 2 : 4;
+  if (y == nullptr || y == x || y == g || !aligned16(y) || !row_stride_ok(ldy, cfg->D, es) || !aligned16(h0) ||
+      !aligned16(h_last) || !aligned16(states) || ws == nullptr || !aligned16(ws))
+    return MATE_ERR_ARG;
+  if (ws_bytes < mate_gated_scan_workspace_bytes(cfg)) return MATE_ERR_WORKSPACE;
+  p.h0 = h0;
+  p.y = y;
+  p.ldy = ldy;
+  p.h_last = h_last;
+  p.states = states;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  t_launches = 0;
+  const dim3 grid(ceil_div(cfg->D, 256), cfg->B);
+  trace_begin(MATE_K_GATED_SCAN, st);
+  if (cfg->dtype == MATE_BF16) gated_scan_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
+  else gated_scan_kernel<float><<<grid, 256, 0, st>>>(p);
+  MATE_LAUNCH_CHECK();
+  return MATE_OK;
+}
+
+size_t mate_gated_scan_backward_workspace_bytes(const mate_gated_scan_config* cfg) {
+  if (check_gated(cfg) != MATE_OK) return 0;
+  return (size_t)cfg->B * cfg->D * sizeof(float);
+}
+
+mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g, long long ldg, const float* bias,
+                                     const float* states, const void* dy, long long lddy, const float* dh_last,
+                                     void* dx, long long lddx, void* dg, long long lddg, float* dbias, float* dh0,
+                                     const mate_gated_scan_config* cfg, void* ws, size_t ws_bytes,
+                                     mate_stream_t stream) {
+  MATE_TRY(check_gated(cfg));
+  GatedScanParams p{};
+  MATE_TRY(fill_gated(cfg, x, ldx, g, ldg, bias, &p));
+  const int es = cfg->dtype == MATE_BF16 ? 2 : 4;
+  if (states == nullptr || dy == nullptr || dx == nullptr || dg == nullptr || ws == nullptr || !aligned16(states) ||
+      !aligned16(dy) || !aligned16(dx) || !aligned16(dg) || !aligned16(dh_last) || !aligned16(dbias) ||
+      !aligned16(dh0) || !aligned16(ws) || !row_stride_ok(lddy, cfg->D, es) || !row_stride_ok(lddx, cfg->D, es) ||
+      !row_stride_ok(lddg, cfg->D, es))
+    return MATE_ERR_ARG;
+  for (const void* in : {x, g, dy})
+    if (dx == in || dg == in) return MATE_ERR_ARG;
+  if (dx == dg) return MATE_ERR_ARG;
+  if (ws_bytes < mate_gated_scan_backward_workspace_bytes(cfg)) return MATE_ERR_WORKSPACE;
+  p.states = const_cast<float*>(states);
+  p.dy = dy;
+  p.lddy = lddy;
+  p.dh_last = dh_last;
+  p.dx = dx;
+  p.lddx = lddx;
+  p.dg = dg;
+  p.lddg = lddg;
+  p.dbias_part = dbias != nullptr ? static_cast<float*>(ws) : nullptr;
+  p.dh0 = dh0;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  t_launches = 0;
+  const dim3 grid(ceil_div(cfg->D, 64), cfg->B);
+  trace_begin(MATE_K_GATED_SCAN_BWD, st);
+  if (cfg->dtype == MATE_BF16) gated_scan_bwd_kernel<__nv_bfloat16><<<grid, 64, 0, st>>>(p);
+  else gated_scan_bwd_kernel<float><<<grid, 64, 0, st>>>(p);
+  MATE_LAUNCH_CHECK();
+  if (dbias != nullptr) {
+    trace_begin(MATE_K_GATED_SCAN_BIAS, st);
+    gated_scan_bias_kernel<<<ceil_div(cfg->D, 256), 256, 0, st>>>(p.dbias_part, cfg->B, cfg->D, dbias);
+    MATE_LAUNCH_CHECK();
+  }
+  return MATE_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------ 8-bit projection
+namespace {
+
+// 2D matrix of bytes [rows, cols], row stride ld (a multiple of 16); box = box_rows x 128 columns, 128B swizzle.
+// Columns and rows behind the matrix read zeros.
+bool make_tmap_s8(CUtensorMap* m, const void* ptr, long long rows, long long cols, long long ld, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+mate_status mate_quantize_rows(const void* x, long long ldx, long long M, int K, mate_dtype dtype, void* q,
+                               long long ldq, float* scale, mate_stream_t stream) {
+  if (dtype != MATE_BF16 && dtype != MATE_F32) return MATE_ERR_ARG;
+  const int es = dtype == MATE_BF16 ? 2 : 4;
+  if (x == nullptr || q == nullptr || scale == nullptr || M < 0 || K <= 0 || M >= (1LL << 31)) return MATE_ERR_ARG;
+  if (!aligned16(x) || !aligned16(q) || (reinterpret_cast<uintptr_t>(scale) & 3u) || !row_stride_ok(ldx, K, es) ||
+      !row_stride_ok(ldq, K, 1))
+    return MATE_ERR_ARG;
+  t_launches = 0;
+  if (M == 0) return MATE_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int blocks = static_cast<int>(std::min<long long>((M + 7) / 8, (long long)device_sms() * 8));
+  trace_begin(MATE_K_QUANTIZE_ROWS, st);
+  if (dtype == MATE_BF16)
+    quantize_rows_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), ldx, M, K,
+                                                                static_cast<int8_t*>(q), ldq, scale);
+  else
+    quantize_rows_kernel<float><<<blocks, 256, 0, st>>>(static_cast<const float*>(x), ldx, M, K,
+                                                        static_cast<int8_t*>(q), ldq, scale);
+  MATE_LAUNCH_CHECK();
+  return MATE_OK;
+}
+
+mate_status mate_project_int8(const void* A, long long lda, const float* a_scale, long long M, int K, const void* Wt,
+                              long long ldw, const float* w_scale, int N, const float* bias, void* C, long long ldc,
+                              mate_dtype out_dtype, mate_stream_t stream) {
+  if (out_dtype != MATE_BF16 && out_dtype != MATE_F32) return MATE_ERR_ARG;
+  if (A == nullptr || a_scale == nullptr || Wt == nullptr || w_scale == nullptr || C == nullptr || M < 0 || K <= 0 ||
+      N <= 0 || M >= (1LL << 31))
+    return MATE_ERR_ARG;
+  if (!aligned16(A) || !aligned16(Wt) || !aligned16(C) || !aligned16(w_scale) || !aligned16(bias) ||
+      (reinterpret_cast<uintptr_t>(a_scale) & 3u) || !row_stride_ok(lda, K, 1) || !row_stride_ok(ldw, K, 1) || ldc < N)
+    return MATE_ERR_ARG;
+  if (K >= 131072) return MATE_ERR_UNSUPPORTED;
+  t_launches = 0;
+  if (M == 0) return MATE_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  Int8GemmParams p;
+  p.M = static_cast<int>(M);
+  p.N = N;
+  p.K = K;
+  p.bn = N >= 256 ? 256 : (N + 31) / 32 * 32;
+  p.num_n_tiles = ceil_div(N, p.bn);
+  const long long tiles = (long long)ceil_div(M, 256) * p.num_n_tiles;
+  if (tiles >= (1LL << 31)) return MATE_ERR_SHAPE;
+  p.num_tiles = static_cast<int>(tiles);
+  p.a_scale = a_scale;
+  p.w_scale = w_scale;
+  p.bias = bias;
+  p.C = C;
+  p.ldc = ldc;
+  p.vec = ldc * (out_dtype == MATE_BF16 ? 2 : 4) % 16 == 0;
+  const uint32_t sb = int8_stage_bytes(p.bn);
+  p.stages = std::min<int>(8, static_cast<int>((kSmemLimit - 1024 - 256) / sb));
+  CUtensorMap ta, tb;
+  if (!make_tmap_s8(&ta, A, M, K, lda, 128) || !make_tmap_s8(&tb, Wt, N, K, ldw, p.bn / 2)) return MATE_ERR_CUDA;
+  const size_t smem = 1024 + (size_t)p.stages * sb + 256;
+  auto kernel = out_dtype == MATE_BF16 ? gemm_int8_pair_kernel<__nv_bfloat16> : gemm_int8_pair_kernel<float>;
+  if (!set_smem(kernel, smem)) return MATE_ERR_CUDA;
+  const int pairs = std::min(p.num_tiles, device_sms() / 2);
+  trace_begin(MATE_K_PROJECT_INT8, st);
+  kernel<<<2 * pairs, kI8Threads, smem, st>>>(ta, tb, p);
+  MATE_LAUNCH_CHECK();
+  return MATE_OK;
+}
+
+}  // extern "C"

@@ -6,7 +6,9 @@ missing, the first call raises ImportError.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import dataclasses
 from typing import Dict, Optional
 
 import torch
@@ -15,7 +17,9 @@ from . import _lib
 
 __all__ = ["MateBlock", "DitBlock", "dit_weights_to_device", "rms_permute", "rms_unpermute", "review_pool", "ssd_scan_bidir", "ssd_scan_bidir_pd",
            "ssd_scan_bidir_noalloc", "ssd_scan_bidir_backward", "tesa_forward", "tesa_backward", "project_bf16", "device_status",
-           "torch_dtype", "weights_to_device", "scan_locality", "KernelTrace"]
+           "torch_dtype", "weights_to_device", "scan_locality", "KernelTrace",
+           "QkConfig", "rope_table", "qk_norm_rope", "qk_norm_rope_backward", "GatedScanConfig", "gated_scan",
+           "gated_scan_states", "gated_scan_backward", "quantize_rows", "project_int8"]
 
 
 def torch_dtype(cfg) -> torch.dtype:
@@ -329,6 +333,308 @@ def project_bf16(A: torch.Tensor, Wt: torch.Tensor, out: Optional[torch.Tensor] 
     st = _lib.load().mate_project_bf16(_p(A), A.stride(0), M, K, _p(Wt), Wt.stride(0), N, _p(out), out.stride(0),
                                        _s(stream))
     _lib.check(st, "mate_project_bf16")
+    return out
+
+
+# ------------------------------------------------------------------------------ operators beside the block
+# They take strided rows, tensors on any CUDA device (which need not be the current one) and an optional stream
+# of that device; what they allocate belongs to the stream they run on.
+def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
+    """Context in which `device` and `stream` are current (nothing to do where they already are)."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int, device, name: str) -> int:
+    """Row stride in elements of a tensor that holds `rows` evenly strided rows of `cols` elements (of one row: any
+    stride that the library takes)."""
+    ok = t.is_cuda and t.dtype == dtype and t.dim() >= 1 and t.shape[-1] == cols and t.numel() == rows * cols and \
+        (t.stride(-1) == 1 or cols == 1) and (device is None or t.device == device)
+    ld, step = cols if rows != 1 else (cols + 15) // 16 * 16, None
+    if ok:
+        for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+            if size == 1:
+                continue
+            if step is None:
+                ld = step = st
+            ok = ok and st == step
+            step *= size
+    if not ok:
+        raise ValueError(f"{name}: expected {rows} evenly strided rows of {cols} {dtype} elements"
+                         f"{'' if device is None else f' on {device}'}, got {t.dtype} {tuple(t.shape)} with strides "
+                         f"{t.stride()} on {t.device}")
+    return ld
+
+
+def _flat(t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, device, name: str):
+    """Pointer of an optional contiguous tensor on `device`."""
+    if t is None:
+        return None
+    _need(t, dtype, numel, name)
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
+    return _p(t)
+
+
+def _workspace(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    """The caller's workspace (uint8, checked), else a new one of the current stream."""
+    if ws is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device or ws.numel() < nbytes:
+        raise ValueError(f"ws: expected at least {nbytes} contiguous uint8 elements on {device}, got {ws.dtype} "
+                         f"{tuple(ws.shape)} on {ws.device}")
+    return ws
+
+
+def _ints(obj, names):
+    """The attributes as C ints (a value that does not fit is refused, not cut)."""
+    vals = [int(getattr(obj, k)) for k in names]
+    for k, v in zip(names, vals):
+        if not -(1 << 31) <= v < (1 << 31):
+            raise ValueError(f"{k} = {v} does not fit a 32-bit int")
+    return vals
+
+
+@dataclasses.dataclass(frozen=True)
+class QkConfig:
+    """Shape of qk_norm_rope's rows: B samples of T x H x W tokens, hq query, hk key and hv value heads of tp channels
+    (tesa_forward's rows: all three th); rt / rh / rw of a head's first channels turn with the token's t / h / w
+    position, in pairs of "adjacent" channels or of the "halves" of each axis' channels."""
+
+    B: int
+    T: int
+    H: int
+    W: int
+    hq: int
+    hk: int
+    hv: int
+    tp: int
+    rt: int = 0
+    rh: int = 0
+    rw: int = 0
+    pairing: str = "adjacent"
+    eps: float = 1e-6
+    dtype: str = "bf16"
+
+    def __post_init__(self):
+        if self.pairing not in ("adjacent", "halves") or self.dtype not in ("bf16", "f32"):
+            raise ValueError(f"pairing {self.pairing!r} (adjacent, halves), dtype {self.dtype!r} (bf16, f32)")
+        c = _lib.CQkConfig(*_ints(self, ("B", "T", "H", "W", "hq", "hk", "hv", "tp", "rt", "rh", "rw")),
+                           int(self.pairing == "halves"), self.eps,
+                           _lib.MATE_BF16 if self.dtype == "bf16" else _lib.MATE_F32)
+        object.__setattr__(self, "ccfg", c)
+
+    @property
+    def rows(self) -> int:
+        return self.B * self.T * self.H * self.W
+
+    @property
+    def width(self) -> int:
+        return (self.hq + self.hk + self.hv) * self.tp
+
+
+def rope_table(count: int, dims: int, start: int = 0, theta: float = 10000.0, device="cuda",
+               stream=None) -> torch.Tensor:
+    """[count, dims / 2, 2] fp32: (cos, sin) of (start + p) theta^(-2 i / dims), the angle in 64 bits (made once)."""
+    device = torch.empty(0, device=device).device
+    with _on(device, stream):
+        tab = torch.empty((max(int(count), 0), max(int(dims), 0) // 2, 2), dtype=torch.float32, device=device)
+        if dims != 0:
+            _lib.check(_lib.load().mate_rope_table(_p(tab), int(start), int(count), int(dims), float(theta), _s(None)),
+                       "mate_rope_table")
+    return tab
+
+
+def _qk_tables(tables, cfg: QkConfig, device):
+    if len(tables) != 3:
+        raise ValueError(f"tables: expected the t, h and w tables, got {len(tables)}")
+    return [None if r == 0 else _flat(t, torch.float32, n * r, device, f"{ax} table")
+            for t, n, r, ax in zip(tables, (cfg.T, cfg.H, cfg.W), (cfg.rt, cfg.rh, cfg.rw), "thw")]
+
+
+def qk_norm_rope(qkv: torch.Tensor, wq: Optional[torch.Tensor], wk: Optional[torch.Tensor], tables, cfg: QkConfig,
+                 out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """RMS norm of every query and key head (weights wq, wk [tp] fp32 or None) and rotation by the token's position,
+    on packed q | k | v rows; value columns pass.  tables: the (t, h, w) tables of rope_table (None for an axis with no
+    channels).  out=qkv works in place."""
+    dt, dev = torch_dtype(cfg), qkv.device
+    ldi = _rows(qkv, dt, cfg.rows, cfg.width, None, "qkv")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty(qkv.shape, dtype=dt, device=dev)
+        ldo = _rows(out, dt, cfg.rows, cfg.width, dev, "out")
+        st = _lib.load().mate_qk_norm_rope(
+            _p(qkv), ldi, _flat(wq, torch.float32, cfg.tp, dev, "wq"), _flat(wk, torch.float32, cfg.tp, dev, "wk"),
+            *_qk_tables(tables, cfg, dev), _p(out), ldo, ctypes.byref(cfg.ccfg), _s(None))
+    _lib.check(st, "mate_qk_norm_rope")
+    return out
+
+
+def qk_norm_rope_backward(qkv: torch.Tensor, wq: Optional[torch.Tensor], wk: Optional[torch.Tensor], tables,
+                          dout: torch.Tensor, cfg: QkConfig, dqkv: Optional[torch.Tensor] = None, ws=None,
+                          stream=None) -> Dict[str, torch.Tensor]:
+    """Gradients of qk_norm_rope from its input and the output gradient: dqkv (may be dout or qkv itself), dwq and dwk
+    [tp] fp32 (summed over rows and heads in a fixed order)."""
+    lib, dt, dev = _lib.load(), torch_dtype(cfg), qkv.device
+    ldi = _rows(qkv, dt, cfg.rows, cfg.width, None, "qkv")
+    ldg = _rows(dout, dt, cfg.rows, cfg.width, dev, "dout")
+    with _on(dev, stream):
+        if dqkv is None:
+            dqkv = torch.empty(qkv.shape, dtype=dt, device=dev)
+        ldd = _rows(dqkv, dt, cfg.rows, cfg.width, dev, "dqkv")
+        dwq = torch.empty(cfg.tp, dtype=torch.float32, device=dev)
+        dwk = torch.empty(cfg.tp, dtype=torch.float32, device=dev)
+        nb = lib.mate_qk_norm_rope_backward_workspace_bytes(ctypes.byref(cfg.ccfg))
+        ws = _workspace(ws, nb, dev)
+        st = lib.mate_qk_norm_rope_backward(
+            _p(qkv), ldi, _flat(wq, torch.float32, cfg.tp, dev, "wq"), _flat(wk, torch.float32, cfg.tp, dev, "wk"),
+            *_qk_tables(tables, cfg, dev), _p(dout), ldg, _p(dqkv), ldd, _p(dwq), _p(dwk), ctypes.byref(cfg.ccfg), _p(ws),
+            ws.numel(), _s(None))
+    _lib.check(st, "mate_qk_norm_rope_backward")
+    return dict(dqkv=dqkv, dwq=dwq, dwk=dwk)
+
+
+@dataclasses.dataclass(frozen=True)
+class GatedScanConfig:
+    """Shape of gated_scan: B samples of T x H x W tokens with D channels, walked along scan order `order` (as
+    rms_permute), from its last position back if `reverse`."""
+
+    B: int
+    T: int
+    H: int
+    W: int
+    D: int
+    order: int = 0
+    reverse: bool = False
+    dtype: str = "bf16"
+
+    def __post_init__(self):
+        if self.dtype not in ("bf16", "f32"):
+            raise ValueError(f"dtype {self.dtype!r} (bf16, f32)")
+        c = _lib.CGatedScanConfig(*_ints(self, ("B", "T", "H", "W", "D", "order")), int(bool(self.reverse)),
+                                  _lib.MATE_BF16 if self.dtype == "bf16" else _lib.MATE_F32)
+        object.__setattr__(self, "ccfg", c)
+
+    @property
+    def rows(self) -> int:
+        return self.B * self.T * self.H * self.W
+
+
+def gated_scan_states(cfg: GatedScanConfig, device="cuda", stream=None) -> torch.Tensor:
+    """Buffer (fp32) for the states that gated_scan leaves for gated_scan_backward."""
+    device = torch.empty(0, device=device).device
+    nb = _lib.load().mate_gated_scan_states_bytes(ctypes.byref(cfg.ccfg))
+    if nb == 0:
+        raise ValueError(f"gated_scan_states: {cfg} is not supported")
+    with _on(device, stream):
+        return torch.empty(nb // 4, dtype=torch.float32, device=device)
+
+
+def gated_scan(x: torch.Tensor, g: torch.Tensor, cfg: GatedScanConfig, bias: Optional[torch.Tensor] = None,
+               h0: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               h_last: Optional[torch.Tensor] = None, states: Optional[torch.Tensor] = None, ws=None, stream=None):
+    """h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(g + bias), along the grid's scan order: (y, h_last).
+    x, g: rows of D channels in grid order (strided rows allowed); bias [D], h0 and h_last [B, D] fp32.
+    states (gated_scan_states): filled for gated_scan_backward."""
+    lib, dt, dev = _lib.load(), torch_dtype(cfg), x.device
+    ldx = _rows(x, dt, cfg.rows, cfg.D, None, "x")
+    ldg = _rows(g, dt, cfg.rows, cfg.D, dev, "g")
+    with _on(dev, stream):
+        if y is None:
+            y = torch.empty(x.shape, dtype=dt, device=dev)
+        if h_last is None:
+            h_last = torch.empty((cfg.B, cfg.D), dtype=torch.float32, device=dev)
+        ldy = _rows(y, dt, cfg.rows, cfg.D, dev, "y")
+        if states is not None:
+            nb = lib.mate_gated_scan_states_bytes(ctypes.byref(cfg.ccfg))
+            _flat(states, torch.float32, nb // 4, dev, "states")
+        ws = _workspace(ws, lib.mate_gated_scan_workspace_bytes(ctypes.byref(cfg.ccfg)), dev)
+        st = lib.mate_gated_scan(_p(x), ldx, _p(g), ldg, _flat(bias, torch.float32, cfg.D, dev, "bias"),
+                                 _flat(h0, torch.float32, cfg.B * cfg.D, dev, "h0"), _p(y), ldy,
+                                 _flat(h_last, torch.float32, cfg.B * cfg.D, dev, "h_last"), _p(states),
+                                 ctypes.byref(cfg.ccfg), _p(ws), ws.numel(), _s(None))
+    _lib.check(st, "mate_gated_scan")
+    return y, h_last
+
+
+def gated_scan_backward(x: torch.Tensor, g: torch.Tensor, states: torch.Tensor, dy: torch.Tensor, cfg: GatedScanConfig,
+                        bias: Optional[torch.Tensor] = None, dh_last: Optional[torch.Tensor] = None,
+                        dx: Optional[torch.Tensor] = None, dg: Optional[torch.Tensor] = None, ws=None,
+                        stream=None) -> Dict[str, torch.Tensor]:
+    """Gradients of gated_scan from its inputs, the states it left and the gradients dy of y and dh_last of h_last
+    (None: zero): dx, dg, dh0 [B, D] and, with a bias, dbias [D]."""
+    lib, dt, dev = _lib.load(), torch_dtype(cfg), x.device
+    ldx = _rows(x, dt, cfg.rows, cfg.D, None, "x")
+    ldg = _rows(g, dt, cfg.rows, cfg.D, dev, "g")
+    lddy = _rows(dy, dt, cfg.rows, cfg.D, dev, "dy")
+    with _on(dev, stream):
+        dx = torch.empty(x.shape, dtype=dt, device=dev) if dx is None else dx
+        dg = torch.empty(g.shape, dtype=dt, device=dev) if dg is None else dg
+        grads = dict(dx=dx, dg=dg, dh0=torch.empty((cfg.B, cfg.D), dtype=torch.float32, device=dev))
+        if bias is not None:
+            grads["dbias"] = torch.empty(cfg.D, dtype=torch.float32, device=dev)
+        nb = lib.mate_gated_scan_states_bytes(ctypes.byref(cfg.ccfg))
+        ws = _workspace(ws, lib.mate_gated_scan_backward_workspace_bytes(ctypes.byref(cfg.ccfg)), dev)
+        st = lib.mate_gated_scan_backward(
+            _p(x), ldx, _p(g), ldg, _flat(bias, torch.float32, cfg.D, dev, "bias"),
+            _flat(states, torch.float32, nb // 4, dev, "states"), _p(dy), lddy,
+            _flat(dh_last, torch.float32, cfg.B * cfg.D, dev, "dh_last"), _p(dx), _rows(dx, dt, cfg.rows, cfg.D, dev, "dx"),
+            _p(dg), _rows(dg, dt, cfg.rows, cfg.D, dev, "dg"), _p(grads.get("dbias")), _p(grads["dh0"]),
+            ctypes.byref(cfg.ccfg), _p(ws), ws.numel(), _s(None))
+    _lib.check(st, "mate_gated_scan_backward")
+    return grads
+
+
+def _mate_dtype(dtype: torch.dtype, name: str) -> int:
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name}: expected torch.bfloat16 or torch.float32, got {dtype}")
+    return _lib.MATE_BF16 if dtype == torch.bfloat16 else _lib.MATE_F32
+
+
+def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None, stream=None):
+    """x [M, K] bf16 or fp32 (strided rows allowed) -> (q [M, K] int8, scale [M] fp32): scale = max|x| / 127 of the row,
+    q = x / scale to the nearest integer, ties to even.  A new q has its rows padded to a multiple of 16 bytes."""
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [M, K], got {tuple(x.shape)}")
+    (M, K), dev, code = x.shape, x.device, _mate_dtype(x.dtype, "x")
+    ldx = _rows(x, x.dtype, M, K, None, "x")
+    with _on(dev, stream):
+        if q is None:
+            ldq = (K + 15) // 16 * 16
+            q = torch.empty((M, ldq), dtype=torch.int8, device=dev)
+            q = q if ldq == K else q[:, :K]
+        if scale is None:
+            scale = torch.empty(M, dtype=torch.float32, device=dev)
+        ldq = _rows(q, torch.int8, M, K, dev, "q")
+        st = _lib.load().mate_quantize_rows(_p(x), ldx, M, K, code, _p(q), ldq,
+                                            _flat(scale, torch.float32, M, dev, "scale"), _s(None)) if M else 0
+    _lib.check(st, "mate_quantize_rows")
+    return q, scale
+
+
+def project_int8(A: torch.Tensor, a_scale: torch.Tensor, Wt: torch.Tensor, w_scale: torch.Tensor,
+                 bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+    """C = (A W^T) a_scale[row] w_scale[column] + bias on tensor cores: A [M, K] and Wt [N, K] int8 (rows on 16 bytes),
+    a_scale [M], w_scale [N], bias [N] fp32 -> C [M, N] bf16 or fp32.  The integer sums are exact."""
+    if A.dim() != 2 or Wt.dim() != 2:
+        raise ValueError(f"A and Wt: expected [M, K] and [N, K], got {tuple(A.shape)} and {tuple(Wt.shape)}")
+    (M, K), N, dev = A.shape, Wt.shape[0], A.device
+    lda = _rows(A, torch.int8, M, K, None, "A")
+    ldw = _rows(Wt, torch.int8, N, K, dev, "Wt")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype, device=dev)
+        code = _mate_dtype(out.dtype, "out")
+        ldc = _rows(out, out.dtype, M, N, dev, "out")
+        st = _lib.load().mate_project_int8(
+            _p(A), lda, _flat(a_scale, torch.float32, M, dev, "a_scale"), M, K, _p(Wt), ldw,
+            _flat(w_scale, torch.float32, N, dev, "w_scale"), N, _flat(bias, torch.float32, N, dev, "bias"), _p(out), ldc,
+            code, _s(None)) if M else 0
+    _lib.check(st, "mate_project_int8")
     return out
 
 
