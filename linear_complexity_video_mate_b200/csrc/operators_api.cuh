@@ -158,8 +158,13 @@ mate_status check_gated(const mate_gated_scan_config* c) {
   if (c->D % (c->dtype == MATE_BF16 ? 8 : 4)) return MATE_ERR_SHAPE;
   const long long hw = (long long)c->H * c->W;
   if (hw >= (1LL << 31) || hw * c->T >= (1LL << 31) || hw * c->T * c->B >= (1LL << 31)) return MATE_ERR_SHAPE;
+  // tiles are counted in 31 bits (a block looks one ticket ahead)
+  const long long tiles = (long long)ceil_div(hw * c->T, kGsRows) * c->B;
+  if (tiles * ceil_div(c->D, kGsChan) >= (1LL << 31)) return MATE_ERR_SHAPE;
   return MATE_OK;
 }
+
+int gated_tiles(const mate_gated_scan_config* c) { return ceil_div((long long)c->T * c->H * c->W, kGsRows); }
 
 mate_status fill_gated(const mate_gated_scan_config* c, const void* x, long long ldx, const void* g, long long ldg,
                        const float* bias, GatedScanParams* p) {
@@ -179,10 +184,53 @@ mate_status fill_gated(const mate_gated_scan_config* c, const void* x, long long
   p->D = c->D;
   p->order = c->order;
   p->reverse = c->reverse;
+  p->n = c->T * c->H * c->W;
+  p->tiles = gated_tiles(c);
+  p->cblocks = ceil_div(c->D, kGsChan);
   return MATE_OK;
 }
 
-int gated_chunks(const mate_gated_scan_config* c) { return ceil_div((long long)c->T * c->H * c->W, kGsChunk); }
+struct GatedScanScratch {
+  unsigned* sync;             // the ticket counter and the abort word
+  unsigned long long *pair, *group;
+  size_t bytes;               // of all that a call fills with ones first
+  float* dbias_part;
+  size_t total;
+};
+
+// A sequence of one tile joins nothing and needs no scratch but the partial bias sums.
+GatedScanScratch carve_gated(const mate_gated_scan_config* c, void* ws, bool backward) {
+  GatedScanScratch s{};
+  Carver cv{static_cast<char*>(ws)};
+  const size_t tiles = gated_tiles(c), row = (size_t)c->B * c->D;
+  s.sync = cv.take<unsigned>(64);
+  if (tiles > 1) {
+    s.pair = cv.take<unsigned long long>((tiles - 1) * row);
+    s.group = cv.take<unsigned long long>(((tiles - 1) / kGsGroup + 1) * row);
+  }
+  s.bytes = cv.off;
+  if (backward) s.dbias_part = cv.take<float>(tiles * row);
+  s.total = cv.off + 256;
+  return s;
+}
+
+// Launches a scan kernel over all tiles, after filling the scratch that the tiles publish in.
+mate_status launch_gated(void (*kernel)(GatedScanParams), int kid, size_t smem, int per_sm, GatedScanParams p,
+                         const GatedScanScratch& s, void* ws, cudaStream_t st) {
+  if (p.tiles > 1) {
+    if (!cuda_ok(cudaMemsetAsync(ws, 0xff, s.bytes, st))) return MATE_ERR_CUDA;
+    p.ticket = s.sync;
+    p.abort = s.sync + 32;
+    p.pair = s.pair;
+    p.group = s.group;
+  }
+  if (!set_smem(kernel, smem)) return MATE_ERR_CUDA;
+  const long long total = (long long)p.tiles * p.B * p.cblocks;
+  trace_begin(kid, st);
+  kernel<<<static_cast<int>(std::min<long long>(total, (long long)per_sm * device_sms())), kGsThreads, smem, st>>>(p);
+  MATE_LAUNCH_CHECK();
+  return MATE_OK;
+}
 
 }  // namespace
 
@@ -190,12 +238,12 @@ extern "C" {
 
 size_t mate_gated_scan_workspace_bytes(const mate_gated_scan_config* cfg) {
   if (check_gated(cfg) != MATE_OK) return 0;
-  return 256;
+  return carve_gated(cfg, nullptr, false).total;
 }
 
 size_t mate_gated_scan_states_bytes(const mate_gated_scan_config* cfg) {
   if (check_gated(cfg) != MATE_OK) return 0;
-  return (size_t)cfg->B * gated_chunks(cfg) * cfg->D * sizeof(float);
+  return (size_t)cfg->B * gated_tiles(cfg) * cfg->D * sizeof(float);
 }
 
 mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long long ldg, const float* bias,
@@ -216,17 +264,24 @@ mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long lo
   p.states = states;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   t_launches = 0;
-  const dim3 grid(ceil_div(cfg->D, 256), cfg->B);
-  trace_begin(MATE_K_GATED_SCAN, st);
-  if (cfg->dtype == MATE_BF16) gated_scan_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(p);
-  else gated_scan_kernel<float><<<grid, 256, 0, st>>>(p);
-  MATE_LAUNCH_CHECK();
-  return MATE_OK;
+  const bool bf = cfg->dtype == MATE_BF16;
+  if (p.n <= kGsShort) {
+    const long long threads = (long long)cfg->B * (cfg->D / 2);
+    const int blocks = static_cast<int>((threads + 127) / 128);
+    trace_begin(MATE_K_GATED_SCAN, st);
+    if (bf) gated_scan_short_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(p);
+    else gated_scan_short_kernel<float><<<blocks, 128, 0, st>>>(p);
+    MATE_LAUNCH_CHECK();
+    return MATE_OK;
+  }
+  return launch_gated(bf ? gated_scan_kernel<__nv_bfloat16> : gated_scan_kernel<float>, MATE_K_GATED_SCAN,
+                      bf ? sizeof(GsSmem<__nv_bfloat16, 2>) : sizeof(GsSmem<float, 2>), bf ? 4 : 3, p,
+                      carve_gated(cfg, ws, false), ws, st);
 }
 
 size_t mate_gated_scan_backward_workspace_bytes(const mate_gated_scan_config* cfg) {
   if (check_gated(cfg) != MATE_OK) return 0;
-  return (size_t)cfg->B * cfg->D * sizeof(float);
+  return carve_gated(cfg, nullptr, true).total;
 }
 
 mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g, long long ldg, const float* bias,
@@ -255,18 +310,17 @@ mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g
   p.lddx = lddx;
   p.dg = dg;
   p.lddg = lddg;
-  p.dbias_part = dbias != nullptr ? static_cast<float*>(ws) : nullptr;
+  const GatedScanScratch s = carve_gated(cfg, ws, true);
+  p.dbias_part = dbias != nullptr ? s.dbias_part : nullptr;
   p.dh0 = dh0;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   t_launches = 0;
-  const dim3 grid(ceil_div(cfg->D, 64), cfg->B);
-  trace_begin(MATE_K_GATED_SCAN_BWD, st);
-  if (cfg->dtype == MATE_BF16) gated_scan_bwd_kernel<__nv_bfloat16><<<grid, 64, 0, st>>>(p);
-  else gated_scan_bwd_kernel<float><<<grid, 64, 0, st>>>(p);
-  MATE_LAUNCH_CHECK();
+  const bool bf = cfg->dtype == MATE_BF16;
+  MATE_TRY(launch_gated(bf ? gated_scan_bwd_kernel<__nv_bfloat16> : gated_scan_bwd_kernel<float>, MATE_K_GATED_SCAN_BWD,
+                        bf ? sizeof(GsSmem<__nv_bfloat16, 3>) : sizeof(GsSmem<float, 3>), bf ? 3 : 2, p, s, ws, st));
   if (dbias != nullptr) {
     trace_begin(MATE_K_GATED_SCAN_BIAS, st);
-    gated_scan_bias_kernel<<<ceil_div(cfg->D, 256), 256, 0, st>>>(p.dbias_part, cfg->B, cfg->D, dbias);
+    gated_scan_bias_kernel<<<ceil_div(cfg->D, 32), 1024, 0, st>>>(s.dbias_part, cfg->B * p.tiles, cfg->D, dbias);
     MATE_LAUNCH_CHECK();
   }
   return MATE_OK;
