@@ -5,27 +5,37 @@
 //   dx_t = (1 - a_t) l_t,  dg_t = l_t (h_{t-1} - x_t) a_t (1 - a_t),  dbias = sum of dg,  dh0 = m_1.
 // States, gates and sums are fp32; y, dx and dg are rounded once on the way out.
 //
-// One pass over the data.  A tile is kGsRows steps x 64 channels; a run of rows maps the state before it to the state
+// One pass over the data.  A tile is a run of rows x 64 channels; a run of rows maps the state before it to the state
 // behind it by h -> A h + H, and such pairs (A, H) join in order.  Persistent blocks take tiles by ticket (all
-// channels and samples of the first rows, then the next rows), prefetch the next tile's rows into shared memory,
-// form the tile's pair, publish it, and find the state before the tile from the pairs of the tiles before it in its
-// group of kGsGroup tiles and the state before that group, which the last tile of the group before publishes.  The
-// joins are the same ones in the same order on every run, whoever publishes first, so the result is reproducible.
-// A ticket only waits for smaller tickets, and a block works its tickets off in order, so the smallest unfinished
-// tile can always finish: nothing depends on how many blocks run at a time.
+// channels and samples of the first rows, then the next rows).  One warp gathers the next tiles' rows by TMA (four rows
+// per instruction, whatever the scan order) into a ring; all eight form the tile's pair, publish it, and find the
+// state before the tile from the pairs of the tiles before it in its group of kGsGroup tiles and the state before that
+// group, which the last tile of the group before publishes.  (A ninth warp for the loads would leave the others 96
+// registers: five warps on one scheduler.)  The joins are the same ones in the same order on every
+// run, whoever publishes first, so the result is reproducible.  A ticket only waits for smaller tickets, and a block
+// works its tickets off in order, so the smallest unfinished tile can always finish: nothing depends on how many
+// blocks run at a time.
 #pragma once
 #include "common.cuh"
 #include "mamba_extras.cuh"   // to_f32, from_f32
 
 namespace mate {
 
-constexpr int kGsRows = 64;            // steps per tile; the forward's `states` hold the state before each tile
 constexpr int kGsChan = 64;            // channels per tile: 32 lanes x 2
 constexpr int kGsWarps = 8;
 constexpr int kGsThreads = kGsWarps * 32;
-constexpr int kGsRun = kGsRows / kGsWarps;   // consecutive steps per thread
+constexpr int kGsLoadWarp = 4;         // the first and the last warp have the tile's total to form
 constexpr int kGsGroup = 32;           // tiles per group: at most 31 pairs to join behind the group's state
 constexpr int kGsShort = 8;            // longest sequence of the short kernel
+
+// Rows per thread and per tile (the forward's `states` hold the state before each tile).  The gates and terms of a
+// thread's rows stay in registers between the two halves of the work.
+template <typename T_>
+constexpr int kGsRun = sizeof(T_) == 2 ? 16 : 8;
+template <typename T_>
+constexpr int kGsRows = kGsWarps * kGsRun<T_>;
+template <typename T_, int NT>
+constexpr int kGsStages = NT == 2 ? 3 : 2;
 
 struct GatedScanParams {
   const void *x, *g;       // rows b*n + raster, strides ldx, ldg
@@ -59,54 +69,82 @@ __device__ __forceinline__ int gs_row(const GatedScanParams& p, int s) {
   return scan_to_raster(p.reverse ? p.n - 1 - s : s, p.T, p.H, p.W, p.order);
 }
 
-// The smaller of sigmoid(z) and sigmoid(-z), with the sign bit set if it is sigmoid(z): one register holds both, each
-// to full precision (the other is one minus it, at least 1/2).
-__device__ __forceinline__ float gs_gate(float z) {
-  const float e = ex2_approx(-1.4426950408889634f * fabsf(z));
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  const float s = e * r;
-  return z < 0.f ? -s : s;
+// Pairs of fp32 values in one instruction each (round to nearest, as the scalar forms).
+__device__ __forceinline__ unsigned long long gs_u64(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
 }
-__device__ __forceinline__ void gs_split(float s, float* a, float* na) {
-  const float t = fabsf(s), u = 1.f - t;
-  const bool neg = __float_as_int(s) < 0;
-  *a = neg ? t : u;
-  *na = neg ? u : t;
+__device__ __forceinline__ float2 gs_f2(unsigned long long v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(gs_u64(a)), "l"(gs_u64(b)), "l"(gs_u64(c)));
+  return gs_f2(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(gs_u64(a)), "l"(gs_u64(b)));
+  return gs_f2(d);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// a = sigmoid(z) and 1 - a, each to full precision: with e = 2^(-z log2 e), held at 2^127 so that it stays finite,
+// a = 1 / (1 + e) (0 where that is below the normal numbers), and 1 - a is e a where a is above 1/2, the difference
+// where it is not.  NaN stays NaN.
+__device__ __forceinline__ void gs_gate(float2 z, float2* a, float2* na) {
+  float2 e = mul_f32x2(z, both(-1.4426950408889634f));
+  asm("min.NaN.f32 %0, %1, 0f42FE0000;" : "=f"(e.x) : "f"(e.x));   // 127
+  asm("min.NaN.f32 %0, %1, 0f42FE0000;" : "=f"(e.y) : "f"(e.y));
+  e.x = ex2_approx(e.x);
+  e.y = ex2_approx(e.y);
+  const float2 d = add2(e, both(1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a->x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a->y) : "f"(d.y));
+  const float2 p = mul_f32x2(e, *a), q = fma2(*a, both(-1.f), both(1.f));
+  na->x = z.x > 0.f ? p.x : q.x;
+  na->y = z.y > 0.f ? p.y : q.y;
 }
 
-__device__ __forceinline__ unsigned long long gs_pack(float lo, float hi) {
-  return (static_cast<unsigned long long>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
+// Data and validity travel in one 64-bit word per channel (A below, H above), so publishing needs no fence and reading
+// no second look.  A vector access is one access per 64-bit element.
+struct GsPair {
+  unsigned long long x, y;   // of a thread's two channels
+};
+__device__ __forceinline__ unsigned long long gs_word(float lo, float hi) { return gs_u64(make_float2(lo, hi)); }
+__device__ __forceinline__ void gs_publish(unsigned long long* w, float2 A, float2 H) {
+  // the low word may not look empty: a NaN gets the payload that arithmetic gives it
+  if (A.x != A.x) A.x = __uint_as_float(0x7fffffffu);
+  if (A.y != A.y) A.y = __uint_as_float(0x7fffffffu);
+  asm volatile("st.relaxed.gpu.global.v2.u64 [%0], {%1, %2};" ::"l"(w), "l"(gs_word(A.x, H.x)), "l"(gs_word(A.y, H.y))
+               : "memory");
 }
-// Data and validity travel in one 64-bit word, so publishing needs no fence and reading no second look.
-__device__ __forceinline__ void gs_publish(unsigned long long* w, unsigned long long v) {
-  asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(w), "l"(v) : "memory");
-}
-__device__ __forceinline__ unsigned long long gs_look(const unsigned long long* w) {
-  unsigned long long v;
-  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(w) : "memory");
+__device__ __forceinline__ GsPair gs_look(const unsigned long long* w) {
+  GsPair v;
+  asm volatile("ld.relaxed.gpu.global.v2.u64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "l"(w) : "memory");
   return v;
+}
+__device__ __forceinline__ bool gs_empty(const GsPair& v) {
+  return static_cast<unsigned>(v.x) == kGsEmpty || static_cast<unsigned>(v.y) == kGsEmpty;
 }
 constexpr unsigned kGsMaxPolls = 1u << 20;   // about a second
 
-// Waits until both words are published; false if the wait ran out here or in another block.
-__device__ __forceinline__ bool gs_wait(const GatedScanParams& p, const unsigned long long* w, unsigned long long v[2]) {
-  for (unsigned i = 0; static_cast<unsigned>(v[0]) == kGsEmpty || static_cast<unsigned>(v[1]) == kGsEmpty; ++i) {
+// Waits until a pair is published; false if the wait ran out here or in another block.
+__device__ __forceinline__ bool gs_wait(const GatedScanParams& p, const unsigned long long* w, GsPair* v) {
+  for (unsigned i = 0; gs_empty(*v); ++i) {
     if (i >= kGsMaxPolls || ((i & 255) == 255 && *reinterpret_cast<volatile unsigned*>(p.abort) != kGsEmpty)) {
       if (i >= kGsMaxPolls) flag_status(MATE_DEV_TIMEOUT);
       *reinterpret_cast<volatile unsigned*>(p.abort) = 0u;
       return false;
     }
     if (i > 8) __nanosleep(32);
-    v[0] = gs_look(w);
-    v[1] = gs_look(w + 1);
+    *v = gs_look(w);
   }
   return true;
 }
-__device__ __forceinline__ float gs_lo(unsigned long long v) { return __uint_as_float(static_cast<unsigned>(v)); }
-__device__ __forceinline__ float gs_hi(unsigned long long v) { return __uint_as_float(static_cast<unsigned>(v >> 32)); }
-// A pair's low word may not look empty: a NaN gets the payload that arithmetic gives it.
-__device__ __forceinline__ float gs_clean(float a) { return a != a ? __uint_as_float(0x7fffffffu) : a; }
 
 template <typename T_>
 __device__ __forceinline__ float2 gs_load2(const T_* p);
@@ -145,338 +183,380 @@ __global__ void __launch_bounds__(128) gated_scan_short_kernel(GatedScanParams p
 #pragma unroll
   for (int s = 0; s < kGsShort; ++s)
     if (s < p.n) {
-      float a, na;
-      gs_split(gs_gate(g[s].x + bias.x), &a, &na);
-      h.x = fmaf(a, h.x, na * x[s].x);
-      gs_split(gs_gate(g[s].y + bias.y), &a, &na);
-      h.y = fmaf(a, h.y, na * x[s].y);
+      float2 a, na;
+      gs_gate(add2(g[s], bias), &a, &na);
+      h = fma2(a, h, mul_f32x2(na, x[s]));
       gs_store2(static_cast<T_*>(p.y) + ((long long)b * p.n + row[s]) * p.ldy + c, h.x, h.y);
     }
   if (p.h_last != nullptr) *reinterpret_cast<float2*>(p.h_last + (long long)b * p.D + c) = h;
 }
 
-// Shared memory of a block: two stages of NT tensors' tiles, then the joins' scratch.
+// Shared memory of a block: a ring of stages with the tiles of NT tensors (x, g and, backward, dy; rows of 64 channels,
+// as the TMA gathers lay them down) and what the tile is, then the joins' scratch.
 template <typename T_, int NT>
 struct GsSmem {
-  T_ tile[2][NT][kGsRows][kGsChan];
-  int row[2][kGsRows];                    // grid row of each step, -1 behind the last
-  float2 wa[kGsWarps][32], wh[kGsWarps][32];   // the warps' pairs (and forward pairs, backward)
-  float2 wf[NT == 3 ? kGsWarps : 1][32];
+  T_ tile[kGsStages<T_, NT>][NT][kGsRows<T_>][kGsChan];
+  int row[kGsStages<T_, NT>][kGsRows<T_>];     // grid row of each step
+  int k[kGsStages<T_, NT>], b[kGsStages<T_, NT>], c0[kGsStages<T_, NT>];   // the tile (in working order), -1: no more
+  float2 wa[kGsWarps][32], wh[kGsWarps][32];   // the warps' pairs (backward: the adjoint's)
+  float2 wf[NT == 3 ? kGsWarps : 1][32];       // backward: the forward pairs' H
   float2 la[kGsWarps][32], lh[kGsWarps][32];   // the pairs that each warp joined from the tiles before
-  float2 lg[32];                          // state before the group
+  float2 lg[32];                               // state before the group
   float2 db[NT == 3 ? kGsWarps : 1][32];
-  unsigned next;
+  uint64_t full[kGsStages<T_, NT>];
 };
 
-struct GsTile {
-  int k, b, c0;   // k-th tile of rows in the order they are worked off
+struct GsMaps {
+  CUtensorMap x, g, dy;   // boxes of one row x 64 channels (fp32: 32), no swizzle
 };
-__device__ __forceinline__ GsTile gs_tile(const GatedScanParams& p, unsigned t) {
-  const unsigned per = static_cast<unsigned>(p.B) * p.cblocks;
-  const unsigned k = t / per, r = t - k * per;
-  return {static_cast<int>(k), static_cast<int>(r / p.cblocks), static_cast<int>(r % p.cblocks) * kGsChan};
+
+// The next ticket of a block, in lane 0 of its loading warp, asked for one tile ahead of its use.  The counter starts at
+// ~0, so that the first ticket is 0; a single tile of rows needs no order.
+__device__ __forceinline__ unsigned gs_ticket(const GatedScanParams& p, unsigned last) {
+  if (p.ticket == nullptr) return last + gridDim.x;
+  return (threadIdx.x & 31) == 0 ? atomicAdd(p.ticket, 1u) + 1u : 0u;
 }
 
-// Copies the rows [k * kGsRows, ..) of the tensors into a stage.
+// Starts the loads of tile t into a stage that no warp reads any more (whole warp); the backward pass (NT = 3) walks the
+// tiles from the last rows to the first.
 template <typename T_, int NT>
-__device__ __forceinline__ void gs_fetch(const GatedScanParams& p, GsSmem<T_, NT>& sm, int stage, int k, int b, int c0) {
-  constexpr int V = 16 / sizeof(T_), PER = kGsChan / V;
+__device__ __forceinline__ void gs_load(const GatedScanParams& p, const GsMaps& maps, GsSmem<T_, NT>& sm, int stage,
+                                        unsigned t) {
+  constexpr int R = kGsRows<T_>, BC = 128 / sizeof(T_);   // channels per gather
+  const int lane = threadIdx.x & 31;
+  const unsigned total = static_cast<unsigned>(p.tiles) * p.B * p.cblocks, per = static_cast<unsigned>(p.B) * p.cblocks;
+  t = __shfl_sync(0xffffffffu, t, 0);
+  const bool more = t < total;
+  const unsigned k = t / per, r = t - k * per;
+  const int b = r / p.cblocks, c0 = (r % p.cblocks) * kGsChan;
+  const int s0 = (NT == 3 ? p.tiles - 1 - static_cast<int>(k) : static_cast<int>(k)) * R;
+  int row[R / 32];
+  if (more) {
 #pragma unroll
-  for (int i = threadIdx.x; i < kGsRows * PER; i += kGsThreads) {
-    const int r = i / PER, v = i % PER, s = k * kGsRows + r;
-    const int row = s < p.n ? gs_row(p, s) : -1;
-    if (v == 0) sm.row[stage][r] = row;
-    const bool ok = row >= 0 && c0 + v * V < p.D;
-    const long long at = (long long)b * p.n + row;
-    cp_async16_zfill(&sm.tile[stage][0][r][v * V], ok ? static_cast<const T_*>(p.x) + at * p.ldx + c0 + v * V : p.x, ok);
-    cp_async16_zfill(&sm.tile[stage][1][r][v * V], ok ? static_cast<const T_*>(p.g) + at * p.ldg + c0 + v * V : p.g, ok);
-    if constexpr (NT == 3)
-      cp_async16_zfill(&sm.tile[stage][2][r][v * V], ok ? static_cast<const T_*>(p.dy) + at * p.lddy + c0 + v * V : p.dy,
-                       ok);
+    for (int j = 0; j < R / 32; ++j) {
+      const int s = s0 + lane * (R / 32) + j;
+      row[j] = s < p.n ? gs_row(p, s) : -1;
+      sm.row[stage][lane * (R / 32) + j] = row[j];
+    }
   }
-  cp_async_commit();
+  if (lane == 0) {
+    sm.k[stage] = more ? static_cast<int>(k) : -1;
+    sm.b[stage] = b;
+    sm.c0[stage] = c0;
+  }
+  __syncwarp();
+  if (lane == 0) {
+    if (more) mbar_arrive_expect_tx(&sm.full[stage], NT * R * kGsChan * sizeof(T_));
+    else mbar_arrive(&sm.full[stage]);
+  }
+  if (!more) return;
+  __syncwarp();
+  // four rows per gather; a row behind the last reads zeros (a row index behind the tensor)
+  const int none = p.B * p.n, base = b * p.n;
+  if constexpr (R / 32 == 4) {
+    const int r0 = row[0] < 0 ? none : base + row[0], r1 = row[1] < 0 ? none : base + row[1];
+    const int r2 = row[2] < 0 ? none : base + row[2], r3 = row[3] < 0 ? none : base + row[3];
+    tma_gather4(&maps.x, &sm.full[stage], &sm.tile[stage][0][lane * 4][0], c0, r0, r1, r2, r3);
+    tma_gather4(&maps.g, &sm.full[stage], &sm.tile[stage][1][lane * 4][0], c0, r0, r1, r2, r3);
+    if constexpr (NT == 3)
+      tma_gather4(&maps.dy, &sm.full[stage], &sm.tile[stage][2][lane * 4][0], c0, r0, r1, r2, r3);
+  } else {
+    // 64 rows of fp32: lane l gathers the rows of lanes 2q, 2q + 1 (q = l / 2), half of the channels (a gather's rows
+    // lie 128 bytes apart, so a tile holds its two halves of 32 channels one behind the other)
+    const int q = lane >> 1, hf = lane & 1;
+    int rr[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int v = __shfl_sync(0xffffffffu, row[j & 1], 2 * q + (j >> 1));
+      rr[j] = v < 0 ? none : base + v;
+    }
+    const int off = hf * R * BC + q * 4 * BC;
+    tma_gather4(&maps.x, &sm.full[stage], &sm.tile[stage][0][0][0] + off, c0 + hf * BC, rr[0], rr[1], rr[2], rr[3]);
+    tma_gather4(&maps.g, &sm.full[stage], &sm.tile[stage][1][0][0] + off, c0 + hf * BC, rr[0], rr[1], rr[2], rr[3]);
+    if constexpr (NT == 3)
+      tma_gather4(&maps.dy, &sm.full[stage], &sm.tile[stage][2][0][0] + off, c0 + hf * BC, rr[0], rr[1], rr[2], rr[3]);
+  }
+}
+
+// A thread's two channels of row r of a stage's tile.
+template <typename T_, int NT>
+__device__ __forceinline__ float2 gs_elem(const GsSmem<T_, NT>& sm, int stage, int tensor, int r, int lane) {
+  constexpr int BC = 128 / sizeof(T_);
+  const T_* base = &sm.tile[stage][tensor][0][0];
+  return gs_load2(base + ((2 * lane) / BC) * (kGsRows<T_> * BC) + r * BC + (2 * lane) % BC);
 }
 
 // Joins the tiles before tile k of its group: warp w takes tiles 4w .. 4w + 3, the last warp the group's state too.
 // Returns false if a wait ran out.
 template <typename T_, int NT>
-__device__ __forceinline__ bool gs_before(const GatedScanParams& p, GsSmem<T_, NT>& sm, int k, int b, int c, bool live,
+__device__ __forceinline__ bool gs_before(const GatedScanParams& p, GsSmem<T_, NT>& sm, int k, long long at, bool live,
                                           float2 start) {
   constexpr int per = kGsGroup / kGsWarps;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int k0 = k / kGsGroup * kGsGroup, m = k - k0;
-  const long long step = (long long)p.B * p.D, at = (long long)b * p.D + c;
-  float2 A = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
+  const int m = k % kGsGroup, j0 = warp * per;
+  const long long step = (long long)p.B * p.D;
+  float2 A = both(1.f), H = both(0.f);
   bool ok = true;
   if (live) {
-    unsigned long long v[per][2];
+    const unsigned long long* w = p.pair + (k - m + j0) * step + at;
+    GsPair v[per];
 #pragma unroll
     for (int j = 0; j < per; ++j)
-      if (warp * per + j < m) {
-        const unsigned long long* w = p.pair + (k0 + warp * per + j) * step + at;
-        v[j][0] = gs_look(w);
-        v[j][1] = gs_look(w + 1);
-      }
+      if (j0 + j < m) v[j] = gs_look(w + j * step);
     if (warp == kGsWarps - 1) {
-      float2 h = start;
-      if (k0 > 0) {
-        const unsigned long long* w = p.group + (k / kGsGroup) * step + at;
-        unsigned long long g[2] = {gs_look(w), gs_look(w + 1)};
-        ok = gs_wait(p, w, g);
-        h = make_float2(gs_hi(g[0]), gs_hi(g[1]));
+      if (k >= kGsGroup) {
+        const unsigned long long* wg = p.group + (k / kGsGroup) * step + at;
+        GsPair g = gs_look(wg);
+        ok = gs_wait(p, wg, &g);
+        start = make_float2(gs_f2(g.x).y, gs_f2(g.y).y);
       }
-      sm.lg[lane] = h;
+      sm.lg[lane] = start;
     }
 #pragma unroll
     for (int j = 0; j < per; ++j)
-      if (warp * per + j < m && ok) {
-        ok = gs_wait(p, p.pair + (k0 + warp * per + j) * step + at, v[j]);
-        H.x = fmaf(gs_lo(v[j][0]), H.x, gs_hi(v[j][0]));
-        H.y = fmaf(gs_lo(v[j][1]), H.y, gs_hi(v[j][1]));
-        A.x *= gs_lo(v[j][0]);
-        A.y *= gs_lo(v[j][1]);
+      if (j0 + j < m && ok) {
+        ok = gs_wait(p, w + j * step, &v[j]);
+        const float2 u = gs_f2(v[j].x), q = gs_f2(v[j].y);
+        H = fma2(make_float2(u.x, q.x), H, make_float2(u.y, q.y));
+        A = mul_f32x2(A, make_float2(u.x, q.x));
       }
   }
-  sm.la[warp][lane] = A;
-  sm.lh[warp][lane] = H;
+  if (j0 < m) {
+    sm.la[warp][lane] = A;
+    sm.lh[warp][lane] = H;
+  }
   return ok;
 }
 
 // The state before the tile, from what gs_before left.
 template <typename T_, int NT>
 __device__ __forceinline__ float2 gs_carry(const GsSmem<T_, NT>& sm, int k, int lane) {
+  constexpr int per = kGsGroup / kGsWarps;
   float2 h = sm.lg[lane];
-  const int used = (k % kGsGroup + kGsGroup / kGsWarps - 1) / (kGsGroup / kGsWarps);
-  for (int w = 0; w < used; ++w) {
-    h.x = fmaf(sm.la[w][lane].x, h.x, sm.lh[w][lane].x);
-    h.y = fmaf(sm.la[w][lane].y, h.y, sm.lh[w][lane].y);
-  }
+  const int used = (k % kGsGroup + per - 1) / per;
+#pragma unroll
+  for (int w = 0; w < kGsWarps; ++w)
+    if (w < used) h = fma2(sm.la[w][lane], h, sm.lh[w][lane]);
   return h;
 }
 
+template <typename T_, int NT>
+__device__ __forceinline__ void gs_init(GsSmem<T_, NT>& sm, const GsMaps& maps) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGsStages<T_, NT>; ++s) {
+      mbar_init(&sm.full[s], 1);
+    }
+    mbar_fence_init();
+    prefetch_tensormap(&maps.x);
+    prefetch_tensormap(&maps.g);
+    if (NT == 3) prefetch_tensormap(&maps.dy);
+  }
+  __syncthreads();
+}
+
 template <typename T_>
-__global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 2 ? 4 : 3) gated_scan_kernel(const GatedScanParams p) {
+__global__ void __launch_bounds__(kGsThreads, 2)
+    gated_scan_kernel(const __grid_constant__ GsMaps maps, const GatedScanParams p) {
   extern __shared__ __align__(128) uint8_t gs_raw[];
   GsSmem<T_, 2>& sm = *reinterpret_cast<GsSmem<T_, 2>*>(gs_raw);
+  constexpr int RUN = kGsRun<T_>, S = kGsStages<T_, 2>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned total = static_cast<unsigned>(p.tiles) * p.B * p.cblocks;
-  const float2 zero = make_float2(0.f, 0.f);
-  // tickets: the counter starts at ~0, so that the first one is 0; a single tile of rows needs no order
-  if (threadIdx.x == 0) sm.next = p.ticket != nullptr ? atomicAdd(p.ticket, 1u) + 1u : blockIdx.x;
-  __syncthreads();
-  unsigned cur = sm.next;
-  int stage = 0;
-  GsTile t = gs_tile(p, cur);
-  if (cur < total) gs_fetch(p, sm, 0, t.k, t.b, t.c0);
-  __syncthreads();
-  while (cur < total) {
-    if (threadIdx.x == 0) sm.next = p.ticket != nullptr ? atomicAdd(p.ticket, 1u) + 1u : cur + gridDim.x;
-    const int c = t.c0 + 2 * lane;
-    const bool live = c < p.D;
+  gs_init(sm, maps);
+  unsigned ticket = 0;
+  if (warp == kGsLoadWarp) {
+    ticket = gs_ticket(p, blockIdx.x - gridDim.x);
+    for (int s = 0; s < S - 1; ++s) {
+      gs_load(p, maps, sm, s, ticket);
+      ticket = gs_ticket(p, ticket);
+    }
+  }
+  const float2 zero = both(0.f), one = both(1.f);
+  const long long step = (long long)p.B * p.D;
+  bool dead = false;   // a wait ran out: the remaining tiles are only taken off the ring
+  for (int it = 0;; ++it) {
+    const int stage = it % S;
+    if (!mbar_wait(&sm.full[stage], (it / S) & 1)) break;
+    const int k = sm.k[stage];
+    if (k < 0) break;
+    const int b = sm.b[stage], c = sm.c0[stage] + 2 * lane;
+    const bool live = c < p.D && !dead;
+    const long long at = (long long)b * p.D + c;
     const float2 bias = live && p.bias != nullptr ? *reinterpret_cast<const float2*>(p.bias + c) : zero;
-    cp_async_wait<0>();
-    __syncthreads();
-    const unsigned nxt = sm.next;
-    const GsTile u = gs_tile(p, nxt);
-    if (nxt < total) gs_fetch(p, sm, stage ^ 1, u.k, u.b, u.c0);
-    float2 a[kGsRun], v[kGsRun];
-    float2 A = make_float2(1.f, 1.f), H = zero;
+    const int rows = min(RUN, p.n - (k * kGsRows<T_> + warp * RUN));   // of this warp; the rest keep the state
+    float2 a[RUN], v[RUN];
+    float2 A = one, H = zero;
 #pragma unroll
-    for (int r = 0; r < kGsRun; ++r) {
-      const float2 x = gs_load2(&sm.tile[stage][0][warp * kGsRun + r][2 * lane]);
-      const float2 g = gs_load2(&sm.tile[stage][1][warp * kGsRun + r][2 * lane]);
+    for (int r = 0; r < RUN; ++r) {
       float2 na;
-      gs_split(gs_gate(g.x + bias.x), &a[r].x, &na.x);
-      gs_split(gs_gate(g.y + bias.y), &a[r].y, &na.y);
-      v[r] = make_float2(na.x * x.x, na.y * x.y);
-      if (sm.row[stage][warp * kGsRun + r] < 0) {   // behind the last row: the state stays
-        a[r] = make_float2(1.f, 1.f);
+      gs_gate(add2(gs_elem(sm, stage, 1, warp * RUN + r, lane), bias), &a[r], &na);
+      v[r] = mul_f32x2(na, gs_elem(sm, stage, 0, warp * RUN + r, lane));
+      if (r >= rows) {
+        a[r] = one;
         v[r] = zero;
       }
-      H = make_float2(fmaf(a[r].x, H.x, v[r].x), fmaf(a[r].y, H.y, v[r].y));
-      A = make_float2(A.x * a[r].x, A.y * a[r].y);
+      H = fma2(a[r], H, v[r]);
+      A = mul_f32x2(A, a[r]);
     }
     sm.wa[warp][lane] = A;
     sm.wh[warp][lane] = H;
     __syncthreads();
-    // pairs of the warps before this one, and of the whole tile
-    float2 Ab = make_float2(1.f, 1.f), Hb = zero, At = Ab, Ht = zero;
+    if (warp == kGsLoadWarp) {   // all warps are done with the tile before this one: its stage takes the next
+      gs_load(p, maps, sm, (it + S - 1) % S, ticket);
+      ticket = gs_ticket(p, ticket);
+    }
+    // pairs of the warps before this one; the first warp forms the whole tile's
+    float2 Ab = one, Hb = zero;
 #pragma unroll
-    for (int w = 0; w < kGsWarps; ++w) {
-      if (w == warp) {
-        Ab = At;
-        Hb = Ht;
+    for (int w = 0; w < kGsWarps; ++w)
+      if (w < warp || warp == 0) {
+        const float2 aw = sm.wa[w][lane];
+        Hb = fma2(aw, Hb, sm.wh[w][lane]);
+        Ab = mul_f32x2(Ab, aw);
       }
-      const float2 aw = sm.wa[w][lane], hw = sm.wh[w][lane];
-      Ht = make_float2(fmaf(aw.x, Ht.x, hw.x), fmaf(aw.y, Ht.y, hw.y));
-      At = make_float2(At.x * aw.x, At.y * aw.y);
-    }
-    const long long step = (long long)p.B * p.D, at = (long long)t.b * p.D + c;
-    if (warp == 0 && live && t.k + 1 < p.tiles) {
-      gs_publish(p.pair + t.k * step + at, gs_pack(gs_clean(At.x), Ht.x));
-      gs_publish(p.pair + t.k * step + at + 1, gs_pack(gs_clean(At.y), Ht.y));
-    }
+    if (warp == 0 && live && k + 1 < p.tiles) gs_publish(p.pair + k * step + at, Ab, Hb);
     const float2 h0 = live && p.h0 != nullptr ? *reinterpret_cast<const float2*>(p.h0 + at) : zero;
-    if (__syncthreads_or(!gs_before(p, sm, t.k, t.b, c, live, h0))) break;
-    const float2 h_in = gs_carry(sm, t.k, lane);
-    if (warp == 0 && live) {
-      if (p.states != nullptr) *reinterpret_cast<float2*>(p.states + ((long long)t.b * p.tiles + t.k) * p.D + c) = h_in;
-      const float2 out = make_float2(fmaf(At.x, h_in.x, Ht.x), fmaf(At.y, h_in.y, Ht.y));
-      if (t.k + 1 == p.tiles) {
-        if (p.h_last != nullptr) *reinterpret_cast<float2*>(p.h_last + at) = out;
-      } else if ((t.k + 1) % kGsGroup == 0) {
-        gs_publish(p.group + (t.k + 1) / kGsGroup * step + at, gs_pack(0.f, out.x));
-        gs_publish(p.group + (t.k + 1) / kGsGroup * step + at + 1, gs_pack(0.f, out.y));
+    dead = __syncthreads_or(!gs_before(p, sm, k, at, live, h0) || dead);
+    if (!dead && live) {
+      float2 h = gs_carry(sm, k, lane);
+      if (warp == 0) {
+        if (p.states != nullptr) *reinterpret_cast<float2*>(p.states + ((long long)b * p.tiles + k) * p.D + c) = h;
+        const float2 out = fma2(Ab, h, Hb);
+        if (k + 1 == p.tiles) {
+          if (p.h_last != nullptr) *reinterpret_cast<float2*>(p.h_last + at) = out;
+        } else if ((k + 1) % kGsGroup == 0) {
+          gs_publish(p.group + (k + 1) / kGsGroup * step + at, zero, out);
+        }
+      } else {
+        h = fma2(Ab, h, Hb);
       }
-    }
-    if (live) {
-      float2 h = make_float2(fmaf(Ab.x, h_in.x, Hb.x), fmaf(Ab.y, h_in.y, Hb.y));
+      T_* y = static_cast<T_*>(p.y) + (long long)b * p.n * p.ldy + c;
 #pragma unroll
-      for (int r = 0; r < kGsRun; ++r) {
-        h = make_float2(fmaf(a[r].x, h.x, v[r].x), fmaf(a[r].y, h.y, v[r].y));
-        const int row = sm.row[stage][warp * kGsRun + r];
-        if (row >= 0) gs_store2(static_cast<T_*>(p.y) + ((long long)t.b * p.n + row) * p.ldy + c, h.x, h.y);
+      for (int r = 0; r < RUN; ++r) {
+        h = fma2(a[r], h, v[r]);
+        if (r < rows) gs_store2(y + sm.row[stage][warp * RUN + r] * p.ldy, h.x, h.y);
       }
     }
-    cur = nxt;
-    t = u;
-    stage ^= 1;
   }
-  cp_async_wait<0>();
 }
 
 // The backward pass: tiles from the last rows to the first; the state before each row is formed again from the saved
 // state before the tile, the adjoint state joins like the forward's (m -> A m + M from the row behind to the row before).
 template <typename T_>
-__global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 2 ? 3 : 2) gated_scan_bwd_kernel(const GatedScanParams p) {
+__global__ void __launch_bounds__(kGsThreads, 2)
+    gated_scan_bwd_kernel(const __grid_constant__ GsMaps maps, const GatedScanParams p) {
   extern __shared__ __align__(128) uint8_t gs_raw[];
   GsSmem<T_, 3>& sm = *reinterpret_cast<GsSmem<T_, 3>*>(gs_raw);
+  constexpr int RUN = kGsRun<T_>, S = kGsStages<T_, 3>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned total = static_cast<unsigned>(p.tiles) * p.B * p.cblocks;
-  const float2 zero = make_float2(0.f, 0.f);
-  if (threadIdx.x == 0) sm.next = p.ticket != nullptr ? atomicAdd(p.ticket, 1u) + 1u : blockIdx.x;
-  __syncthreads();
-  unsigned cur = sm.next;
-  int stage = 0;
-  GsTile t = gs_tile(p, cur);
-  if (cur < total) gs_fetch(p, sm, 0, p.tiles - 1 - t.k, t.b, t.c0);
-  __syncthreads();
-  while (cur < total) {
-    if (threadIdx.x == 0) sm.next = p.ticket != nullptr ? atomicAdd(p.ticket, 1u) + 1u : cur + gridDim.x;
-    const int kr = p.tiles - 1 - t.k;   // the tile of rows
-    const int c = t.c0 + 2 * lane;
-    const bool live = c < p.D;
-    const long long step = (long long)p.B * p.D, at = (long long)t.b * p.D + c;
+  gs_init(sm, maps);
+  unsigned ticket = 0;
+  if (warp == kGsLoadWarp) {
+    ticket = gs_ticket(p, blockIdx.x - gridDim.x);
+    for (int s = 0; s < S - 1; ++s) {
+      gs_load(p, maps, sm, s, ticket);
+      ticket = gs_ticket(p, ticket);
+    }
+  }
+  const float2 zero = both(0.f), one = both(1.f), neg = both(-1.f);
+  const long long step = (long long)p.B * p.D;
+  bool dead = false;
+  for (int it = 0;; ++it) {
+    const int stage = it % S;
+    if (!mbar_wait(&sm.full[stage], (it / S) & 1)) break;
+    const int k = sm.k[stage];
+    if (k < 0) break;
+    const int kr = p.tiles - 1 - k;   // the tile of rows
+    const int b = sm.b[stage], c = sm.c0[stage] + 2 * lane;
+    const bool live = c < p.D && !dead;
+    const long long at = (long long)b * p.D + c;
     const float2 bias = live && p.bias != nullptr ? *reinterpret_cast<const float2*>(p.bias + c) : zero;
-    const float2 h_in =
-        live ? *reinterpret_cast<const float2*>(p.states + ((long long)t.b * p.tiles + kr) * p.D + c) : zero;
-    cp_async_wait<0>();
-    __syncthreads();
-    const unsigned nxt = sm.next;
-    const GsTile u = gs_tile(p, nxt);
-    if (nxt < total) gs_fetch(p, sm, stage ^ 1, p.tiles - 1 - u.k, u.b, u.c0);
-    float2 s[kGsRun], w[kGsRun];   // gate; first (1 - a) x, then the state before the row minus x
-    float2 A = make_float2(1.f, 1.f), H = zero, Mm = zero;
+    const float2 h_in = live ? *reinterpret_cast<const float2*>(p.states + ((long long)b * p.tiles + kr) * p.D + c) : zero;
+    const int rows = min(RUN, p.n - (kr * kGsRows<T_> + warp * RUN));
+    float2 a[RUN], na[RUN];
+    float2 A = one, H = zero, Mm = zero;
 #pragma unroll
-    for (int r = 0; r < kGsRun; ++r) {
-      const float2 x = gs_load2(&sm.tile[stage][0][warp * kGsRun + r][2 * lane]);
-      const float2 g = gs_load2(&sm.tile[stage][1][warp * kGsRun + r][2 * lane]);
-      s[r] = make_float2(gs_gate(g.x + bias.x), gs_gate(g.y + bias.y));
-      if (sm.row[stage][warp * kGsRun + r] < 0) s[r] = zero;   // behind the last row: a = 1
-      float2 a, na;
-      gs_split(s[r].x, &a.x, &na.x);
-      gs_split(s[r].y, &a.y, &na.y);
-      H = make_float2(fmaf(a.x, H.x, na.x * x.x), fmaf(a.y, H.y, na.y * x.y));
-      A = make_float2(A.x * a.x, A.y * a.y);
+    for (int r = 0; r < RUN; ++r) {
+      gs_gate(add2(gs_elem(sm, stage, 1, warp * RUN + r, lane), bias), &a[r], &na[r]);
+      if (r >= rows) {
+        a[r] = one;
+        na[r] = zero;
+      }
+      H = fma2(a[r], H, mul_f32x2(na[r], gs_elem(sm, stage, 0, warp * RUN + r, lane)));
+      A = mul_f32x2(A, a[r]);
     }
 #pragma unroll
-    for (int r = kGsRun - 1; r >= 0; --r) {
-      const float2 dy = gs_load2(&sm.tile[stage][2][warp * kGsRun + r][2 * lane]);
-      float2 a, na;
-      gs_split(s[r].x, &a.x, &na.x);
-      gs_split(s[r].y, &a.y, &na.y);
-      Mm = make_float2(a.x * (dy.x + Mm.x), a.y * (dy.y + Mm.y));
-    }
+    for (int r = RUN - 1; r >= 0; --r) Mm = mul_f32x2(a[r], add2(gs_elem(sm, stage, 2, warp * RUN + r, lane), Mm));
     sm.wa[warp][lane] = A;
     sm.wf[warp][lane] = H;
     sm.wh[warp][lane] = Mm;
     __syncthreads();
-    // adjoint pairs of the warps behind this one and of the whole tile; the state before this warp's rows
-    float2 Ab = make_float2(1.f, 1.f), Mb = zero, At = Ab, Mt = zero, h = h_in;
+    if (warp == kGsLoadWarp) {
+      gs_load(p, maps, sm, (it + S - 1) % S, ticket);
+      ticket = gs_ticket(p, ticket);
+    }
+    // adjoint pairs of the warps behind this one (the last warp: of the whole tile); the state before this warp's rows
+    float2 Ab = one, Mb = zero, h = h_in;
 #pragma unroll
-    for (int q = kGsWarps - 1; q >= 0; --q) {
-      if (q == warp) {
-        Ab = At;
-        Mb = Mt;
+    for (int q = kGsWarps - 1; q >= 0; --q)
+      if (q > warp || warp == kGsWarps - 1) {
+        const float2 aw = sm.wa[q][lane];
+        Mb = fma2(aw, Mb, sm.wh[q][lane]);
+        Ab = mul_f32x2(Ab, aw);
       }
-      const float2 aw = sm.wa[q][lane], mw = sm.wh[q][lane];
-      Mt = make_float2(fmaf(aw.x, Mt.x, mw.x), fmaf(aw.y, Mt.y, mw.y));
-      At = make_float2(At.x * aw.x, At.y * aw.y);
-    }
-    if (warp == 0 && live && t.k + 1 < p.tiles) {
-      gs_publish(p.pair + t.k * step + at, gs_pack(gs_clean(At.x), Mt.x));
-      gs_publish(p.pair + t.k * step + at + 1, gs_pack(gs_clean(At.y), Mt.y));
-    }
+    if (warp == kGsWarps - 1 && live && k + 1 < p.tiles) gs_publish(p.pair + k * step + at, Ab, Mb);
 #pragma unroll
     for (int q = 0; q < kGsWarps - 1; ++q)
-      if (q < warp) {
-        const float2 aw = sm.wa[q][lane], hw = sm.wf[q][lane];
-        h = make_float2(fmaf(aw.x, h.x, hw.x), fmaf(aw.y, h.y, hw.y));
-      }
-#pragma unroll
-    for (int r = 0; r < kGsRun; ++r) {
-      const float2 x = gs_load2(&sm.tile[stage][0][warp * kGsRun + r][2 * lane]);
-      w[r] = make_float2(h.x - x.x, h.y - x.y);
-      float2 a, na;
-      gs_split(s[r].x, &a.x, &na.x);
-      gs_split(s[r].y, &a.y, &na.y);
-      h = make_float2(fmaf(a.x, h.x, na.x * x.x), fmaf(a.y, h.y, na.y * x.y));
-    }
+      if (q < warp) h = fma2(sm.wa[q][lane], h, sm.wf[q][lane]);
     const float2 m0 = live && p.dh_last != nullptr ? *reinterpret_cast<const float2*>(p.dh_last + at) : zero;
-    if (__syncthreads_or(!gs_before(p, sm, t.k, t.b, c, live, m0))) break;
-    const float2 m_in = gs_carry(sm, t.k, lane);
-    if (warp == 0 && live) {
-      const float2 out = make_float2(fmaf(At.x, m_in.x, Mt.x), fmaf(At.y, m_in.y, Mt.y));
-      if (t.k + 1 == p.tiles) {
-        if (p.dh0 != nullptr) *reinterpret_cast<float2*>(p.dh0 + at) = out;
-      } else if ((t.k + 1) % kGsGroup == 0) {
-        gs_publish(p.group + (t.k + 1) / kGsGroup * step + at, gs_pack(0.f, out.x));
-        gs_publish(p.group + (t.k + 1) / kGsGroup * step + at + 1, gs_pack(0.f, out.y));
+    dead = __syncthreads_or(!gs_before(p, sm, k, at, live, m0) || dead);
+    float2 db = zero;
+    if (!dead && live) {
+      float2 m = gs_carry(sm, k, lane);
+      if (warp == kGsWarps - 1) {
+        const float2 out = fma2(Ab, m, Mb);
+        if (k + 1 == p.tiles) {
+          if (p.dh0 != nullptr) *reinterpret_cast<float2*>(p.dh0 + at) = out;
+        } else if ((k + 1) % kGsGroup == 0) {
+          gs_publish(p.group + (k + 1) / kGsGroup * step + at, zero, out);
+        }
+      } else {
+        m = fma2(Ab, m, Mb);
       }
-    }
-    float2 m = make_float2(fmaf(Ab.x, m_in.x, Mb.x), fmaf(Ab.y, m_in.y, Mb.y)), db = zero;
+      // the state before each row, less x
+      float2 w[RUN];
 #pragma unroll
-    for (int r = kGsRun - 1; r >= 0; --r) {
-      const float2 dy = gs_load2(&sm.tile[stage][2][warp * kGsRun + r][2 * lane]);
-      const float2 l = make_float2(dy.x + m.x, dy.y + m.y);
-      float2 a, na;
-      gs_split(s[r].x, &a.x, &na.x);
-      gs_split(s[r].y, &a.y, &na.y);
-      const float2 dg = make_float2(l.x * w[r].x * (a.x * na.x), l.y * w[r].y * (a.y * na.y));
-      m = make_float2(a.x * l.x, a.y * l.y);
-      const int row = sm.row[stage][warp * kGsRun + r];
-      if (row >= 0 && live) {
-        const long long o = (long long)t.b * p.n + row;
-        gs_store2(static_cast<T_*>(p.dx) + o * p.lddx + c, na.x * l.x, na.y * l.y);
-        gs_store2(static_cast<T_*>(p.dg) + o * p.lddg + c, dg.x, dg.y);
-        db = make_float2(db.x + dg.x, db.y + dg.y);
+      for (int r = 0; r < RUN; ++r) {
+        const float2 x = gs_elem(sm, stage, 0, warp * RUN + r, lane);
+        w[r] = fma2(x, neg, h);
+        h = fma2(a[r], h, mul_f32x2(na[r], x));
+      }
+      T_* dx = static_cast<T_*>(p.dx) + (long long)b * p.n * p.lddx + c;
+      T_* dg = static_cast<T_*>(p.dg) + (long long)b * p.n * p.lddg + c;
+#pragma unroll
+      for (int r = RUN - 1; r >= 0; --r) {
+        const float2 l = add2(gs_elem(sm, stage, 2, warp * RUN + r, lane), m);
+        const float2 o = mul_f32x2(na[r], l);
+        m = mul_f32x2(a[r], l);
+        const float2 d = mul_f32x2(mul_f32x2(o, w[r]), a[r]);
+        if (r < rows) {
+          const int row = sm.row[stage][warp * RUN + r];
+          gs_store2(dx + row * p.lddx, o.x, o.y);
+          gs_store2(dg + row * p.lddg, d.x, d.y);
+          db = add2(db, d);
+        }
       }
     }
     if (p.dbias_part != nullptr) {
       sm.db[warp][lane] = db;
       __syncthreads();
-      if (warp == 0 && live) {
+      if (warp == 0 && live && !dead) {
         float2 v = zero;
 #pragma unroll
-        for (int q = 0; q < kGsWarps; ++q) v = make_float2(v.x + sm.db[q][lane].x, v.y + sm.db[q][lane].y);
-        *reinterpret_cast<float2*>(p.dbias_part + ((long long)t.b * p.tiles + kr) * p.D + c) = v;
+        for (int q = 0; q < kGsWarps; ++q) v = add2(v, sm.db[q][lane]);
+        *reinterpret_cast<float2*>(p.dbias_part + ((long long)b * p.tiles + kr) * p.D + c) = v;
       }
     }
-    cur = nxt;
-    t = u;
-    stage ^= 1;
   }
-  cp_async_wait<0>();
 }
 
 // dbias [D] = the tiles' partial sums, added in their order (the same result on every run): a block takes 32 channels,

@@ -159,12 +159,14 @@ mate_status check_gated(const mate_gated_scan_config* c) {
   const long long hw = (long long)c->H * c->W;
   if (hw >= (1LL << 31) || hw * c->T >= (1LL << 31) || hw * c->T * c->B >= (1LL << 31)) return MATE_ERR_SHAPE;
   // tiles are counted in 31 bits (a block looks one ticket ahead)
-  const long long tiles = (long long)ceil_div(hw * c->T, kGsRows) * c->B;
+  const long long tiles = (long long)ceil_div(hw * c->T, kGsRows<float>) * c->B;
   if (tiles * ceil_div(c->D, kGsChan) >= (1LL << 31)) return MATE_ERR_SHAPE;
   return MATE_OK;
 }
 
-int gated_tiles(const mate_gated_scan_config* c) { return ceil_div((long long)c->T * c->H * c->W, kGsRows); }
+int gated_tiles(const mate_gated_scan_config* c) {
+  return ceil_div((long long)c->T * c->H * c->W, c->dtype == MATE_BF16 ? kGsRows<__nv_bfloat16> : kGsRows<float>);
+}
 
 mate_status fill_gated(const mate_gated_scan_config* c, const void* x, long long ldx, const void* g, long long ldg,
                        const float* bias, GatedScanParams* p) {
@@ -214,8 +216,22 @@ GatedScanScratch carve_gated(const mate_gated_scan_config* c, void* ws, bool bac
   return s;
 }
 
+// Rows of 128 bytes' worth of channels for the gathers (rows are picked one by one; behind the matrix zeros).
+bool make_tmap_rows(CUtensorMap* m, const void* ptr, long long rows, int cols, long long ld, bool bf16) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const int es = bf16 ? 2 : 4;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), 1};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(ptr), dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Launches a scan kernel over all tiles, after filling the scratch that the tiles publish in.
-mate_status launch_gated(void (*kernel)(GatedScanParams), int kid, size_t smem, int per_sm, GatedScanParams p,
+mate_status launch_gated(void (*kernel)(GsMaps, GatedScanParams), int kid, size_t smem, GatedScanParams p, bool bf16,
                          const GatedScanScratch& s, void* ws, cudaStream_t st) {
   if (p.tiles > 1) {
     if (!cuda_ok(cudaMemsetAsync(ws, 0xff, s.bytes, st))) return MATE_ERR_CUDA;
@@ -224,10 +240,16 @@ mate_status launch_gated(void (*kernel)(GatedScanParams), int kid, size_t smem, 
     p.pair = s.pair;
     p.group = s.group;
   }
+  GsMaps maps;
+  const long long rows = (long long)p.B * p.n;
+  if (!make_tmap_rows(&maps.x, p.x, rows, p.D, p.ldx, bf16) || !make_tmap_rows(&maps.g, p.g, rows, p.D, p.ldg, bf16) ||
+      (p.dy != nullptr && !make_tmap_rows(&maps.dy, p.dy, rows, p.D, p.lddy, bf16)))
+    return MATE_ERR_CUDA;
+  if (p.dy == nullptr) maps.dy = maps.x;   // never read
   if (!set_smem(kernel, smem)) return MATE_ERR_CUDA;
   const long long total = (long long)p.tiles * p.B * p.cblocks;
   trace_begin(kid, st);
-  kernel<<<static_cast<int>(std::min<long long>(total, (long long)per_sm * device_sms())), kGsThreads, smem, st>>>(p);
+  kernel<<<static_cast<int>(std::min<long long>(total, 2LL * device_sms())), kGsThreads, smem, st>>>(maps, p);
   MATE_LAUNCH_CHECK();
   return MATE_OK;
 }
@@ -275,7 +297,7 @@ mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long lo
     return MATE_OK;
   }
   return launch_gated(bf ? gated_scan_kernel<__nv_bfloat16> : gated_scan_kernel<float>, MATE_K_GATED_SCAN,
-                      bf ? sizeof(GsSmem<__nv_bfloat16, 2>) : sizeof(GsSmem<float, 2>), bf ? 4 : 3, p,
+                      bf ? sizeof(GsSmem<__nv_bfloat16, 2>) : sizeof(GsSmem<float, 2>), p, bf,
                       carve_gated(cfg, ws, false), ws, st);
 }
 
@@ -317,7 +339,7 @@ mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g
   t_launches = 0;
   const bool bf = cfg->dtype == MATE_BF16;
   MATE_TRY(launch_gated(bf ? gated_scan_bwd_kernel<__nv_bfloat16> : gated_scan_bwd_kernel<float>, MATE_K_GATED_SCAN_BWD,
-                        bf ? sizeof(GsSmem<__nv_bfloat16, 3>) : sizeof(GsSmem<float, 3>), bf ? 3 : 2, p, s, ws, st));
+                        bf ? sizeof(GsSmem<__nv_bfloat16, 3>) : sizeof(GsSmem<float, 3>), p, bf, s, ws, st));
   if (dbias != nullptr) {
     trace_begin(MATE_K_GATED_SCAN_BIAS, st);
     gated_scan_bias_kernel<<<ceil_div(cfg->D, 32), 1024, 0, st>>>(s.dbias_part, cfg->B * p.tiles, cfg->D, dbias);
