@@ -92,22 +92,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
-// a = sigmoid(z) and 1 - a, each to full precision: with e = 2^(-z log2 e), held at 2^127 so that it stays finite,
-// a = 1 / (1 + e) (0 where that is below the normal numbers), and 1 - a is e a where a is above 1/2, the difference
-// where it is not.  NaN stays NaN.
-__device__ __forceinline__ void gs_gate(float2 z, float2* a, float2* na) {
-  float2 e = mul_f32x2(z, both(-1.4426950408889634f));
-  asm("min.NaN.f32 %0, %1, 0f42FE0000;" : "=f"(e.x) : "f"(e.x));   // 127
-  asm("min.NaN.f32 %0, %1, 0f42FE0000;" : "=f"(e.y) : "f"(e.y));
-  e.x = ex2_approx(e.x);
-  e.y = ex2_approx(e.y);
+// a = sigmoid(z) and 1 - a, each to full precision, from t = -z log2 e: with e = 2^t, a = 1 / (1 + e) (0 where that is
+// below the normal numbers), and 1 - a is e a where a is above 1/2, the difference where it is not (there e a may be
+// infinity times 0).  NaN stays NaN.
+__device__ __forceinline__ void gs_gate(float2 t, float2* a, float2* na) {
+  const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
   const float2 d = add2(e, both(1.f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a->x) : "f"(d.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(a->y) : "f"(d.y));
   const float2 p = mul_f32x2(e, *a), q = fma2(*a, both(-1.f), both(1.f));
-  na->x = z.x > 0.f ? p.x : q.x;
-  na->y = z.y > 0.f ? p.y : q.y;
+  na->x = t.x < 0.f ? p.x : q.x;
+  na->y = t.y < 0.f ? p.y : q.y;
 }
+constexpr float kGsLog2e = -1.4426950408889634f;
 
 // Data and validity travel in one 64-bit word per channel (A below, H above), so publishing needs no fence and reading
 // no second look.  A vector access is one access per 64-bit element.
@@ -159,6 +156,12 @@ __device__ __forceinline__ void gs_store2(__nv_bfloat16* p, float a, float b) {
   *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(a, b);
 }
 
+// Row `row` behind p; row strides are below 2^31 elements.
+template <typename T_>
+__device__ __forceinline__ T_* gs_at(T_* p, int row, unsigned ld) {
+  return p + static_cast<unsigned long long>(static_cast<unsigned>(row)) * ld;
+}
+
 // Short sequences (a token or a few per call): one thread per sample and channel pair, no tiles.
 template <typename T_>
 __global__ void __launch_bounds__(128) gated_scan_short_kernel(GatedScanParams p) {
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(128) gated_scan_short_kernel(GatedScanParams p
   for (int s = 0; s < kGsShort; ++s)
     if (s < p.n) {
       float2 a, na;
-      gs_gate(add2(g[s], bias), &a, &na);
+      gs_gate(mul_f32x2(add2(g[s], bias), both(kGsLog2e)), &a, &na);
       h = fma2(a, h, mul_f32x2(na, x[s]));
       gs_store2(static_cast<T_*>(p.y) + ((long long)b * p.n + row[s]) * p.ldy + c, h.x, h.y);
     }
@@ -196,7 +199,7 @@ __global__ void __launch_bounds__(128) gated_scan_short_kernel(GatedScanParams p
 template <typename T_, int NT>
 struct GsSmem {
   T_ tile[kGsStages<T_, NT>][NT][kGsRows<T_>][kGsChan];
-  int row[kGsStages<T_, NT>][kGsRows<T_>];     // grid row of each step
+  alignas(16) int row[kGsStages<T_, NT>][kGsRows<T_>];     // grid row of each step
   int k[kGsStages<T_, NT>], b[kGsStages<T_, NT>], c0[kGsStages<T_, NT>];   // the tile (in working order), -1: no more
   float2 wa[kGsWarps][32], wh[kGsWarps][32];   // the warps' pairs (backward: the adjoint's)
   float2 wf[NT == 3 ? kGsWarps : 1][32];       // backward: the forward pairs' H
@@ -381,19 +384,27 @@ __global__ void __launch_bounds__(kGsThreads, 2)
     const int b = sm.b[stage], c = sm.c0[stage] + 2 * lane;
     const bool live = c < p.D && !dead;
     const long long at = (long long)b * p.D + c;
-    const float2 bias = live && p.bias != nullptr ? *reinterpret_cast<const float2*>(p.bias + c) : zero;
-    const int rows = min(RUN, p.n - (k * kGsRows<T_> + warp * RUN));   // of this warp; the rest keep the state
+    const float2 bias = mul_f32x2(
+        live && p.bias != nullptr ? *reinterpret_cast<const float2*>(p.bias + c) : zero, both(kGsLog2e));
+    const int rows = p.n - (k * kGsRows<T_> + warp * RUN);   // of this warp, RUN at most; the rest keep the state
     float2 a[RUN], v[RUN];
     float2 A = one, H = zero;
 #pragma unroll
     for (int r = 0; r < RUN; ++r) {
       float2 na;
-      gs_gate(add2(gs_elem(sm, stage, 1, warp * RUN + r, lane), bias), &a[r], &na);
+      gs_gate(fma2(gs_elem(sm, stage, 1, warp * RUN + r, lane), both(kGsLog2e), bias), &a[r], &na);
       v[r] = mul_f32x2(na, gs_elem(sm, stage, 0, warp * RUN + r, lane));
-      if (r >= rows) {
-        a[r] = one;
-        v[r] = zero;
-      }
+    }
+    if (rows < RUN) {
+#pragma unroll
+      for (int r = 0; r < RUN; ++r)
+        if (r >= rows) {
+          a[r] = one;
+          v[r] = zero;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RUN; ++r) {
       H = fma2(a[r], H, v[r]);
       A = mul_f32x2(A, a[r]);
     }
@@ -430,10 +441,25 @@ __global__ void __launch_bounds__(kGsThreads, 2)
         h = fma2(Ab, h, Hb);
       }
       T_* y = static_cast<T_*>(p.y) + (long long)b * p.n * p.ldy + c;
+      if (rows >= RUN) {
 #pragma unroll
-      for (int r = 0; r < RUN; ++r) {
-        h = fma2(a[r], h, v[r]);
-        if (r < rows) gs_store2(y + sm.row[stage][warp * RUN + r] * p.ldy, h.x, h.y);
+        for (int r = 0; r < RUN; r += 4) {
+          const int4 row = *reinterpret_cast<const int4*>(&sm.row[stage][warp * RUN + r]);
+          h = fma2(a[r], h, v[r]);
+          gs_store2(gs_at(y, row.x, p.ldy), h.x, h.y);
+          h = fma2(a[r + 1], h, v[r + 1]);
+          gs_store2(gs_at(y, row.y, p.ldy), h.x, h.y);
+          h = fma2(a[r + 2], h, v[r + 2]);
+          gs_store2(gs_at(y, row.z, p.ldy), h.x, h.y);
+          h = fma2(a[r + 3], h, v[r + 3]);
+          gs_store2(gs_at(y, row.w, p.ldy), h.x, h.y);
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < RUN; ++r) {
+          h = fma2(a[r], h, v[r]);
+          if (r < rows) gs_store2(gs_at(y, sm.row[stage][warp * RUN + r], p.ldy), h.x, h.y);
+        }
       }
     }
   }
@@ -469,18 +495,25 @@ __global__ void __launch_bounds__(kGsThreads, 2)
     const int b = sm.b[stage], c = sm.c0[stage] + 2 * lane;
     const bool live = c < p.D && !dead;
     const long long at = (long long)b * p.D + c;
-    const float2 bias = live && p.bias != nullptr ? *reinterpret_cast<const float2*>(p.bias + c) : zero;
+    const float2 bias = mul_f32x2(
+        live && p.bias != nullptr ? *reinterpret_cast<const float2*>(p.bias + c) : zero, both(kGsLog2e));
     const float2 h_in = live ? *reinterpret_cast<const float2*>(p.states + ((long long)b * p.tiles + kr) * p.D + c) : zero;
-    const int rows = min(RUN, p.n - (kr * kGsRows<T_> + warp * RUN));
+    const int rows = p.n - (kr * kGsRows<T_> + warp * RUN);
     float2 a[RUN], na[RUN];
     float2 A = one, H = zero, Mm = zero;
 #pragma unroll
+    for (int r = 0; r < RUN; ++r)
+      gs_gate(fma2(gs_elem(sm, stage, 1, warp * RUN + r, lane), both(kGsLog2e), bias), &a[r], &na[r]);
+    if (rows < RUN) {
+#pragma unroll
+      for (int r = 0; r < RUN; ++r)
+        if (r >= rows) {
+          a[r] = one;
+          na[r] = zero;
+        }
+    }
+#pragma unroll
     for (int r = 0; r < RUN; ++r) {
-      gs_gate(add2(gs_elem(sm, stage, 1, warp * RUN + r, lane), bias), &a[r], &na[r]);
-      if (r >= rows) {
-        a[r] = one;
-        na[r] = zero;
-      }
       H = fma2(a[r], H, mul_f32x2(na[r], gs_elem(sm, stage, 0, warp * RUN + r, lane)));
       A = mul_f32x2(A, a[r]);
     }
@@ -540,8 +573,8 @@ __global__ void __launch_bounds__(kGsThreads, 2)
         const float2 d = mul_f32x2(mul_f32x2(o, w[r]), a[r]);
         if (r < rows) {
           const int row = sm.row[stage][warp * RUN + r];
-          gs_store2(dx + row * p.lddx, o.x, o.y);
-          gs_store2(dg + row * p.lddg, d.x, d.y);
+          gs_store2(gs_at(dx, row, p.lddx), o.x, o.y);
+          gs_store2(gs_at(dg, row, p.lddg), d.x, d.y);
           db = add2(db, d);
         }
       }

@@ -26,8 +26,10 @@ mate_status check_qk(const mate_qk_config* c) {
   return MATE_OK;
 }
 
-// Row stride in elements: rows start on 16 bytes and hold `width` elements.
-bool row_stride_ok(long long ld, long long width, int es) { return ld >= width && ld * es % 16 == 0; }
+// Row stride in elements, below 2^31: rows start on 16 bytes and hold `width` elements.
+bool row_stride_ok(long long ld, long long width, int es) {
+  return ld >= width && ld < (1LL << 31) && ld * es % 16 == 0;
+}
 
 mate_status fill_qk(const mate_qk_config* c, const void* x, long long ldx, const float* wq, const float* wk,
                     const float* tt, const float* th, const float* tw, QkParams* p) {
