@@ -33,28 +33,138 @@ __device__ __forceinline__ int quant_round_tiny(float x, float s) {
   return static_cast<int>(fmin(fmax(rint(static_cast<double>(x) / static_cast<double>(s)), -127.0), 127.0));
 }
 
-// One warp per row, 16 bytes of q per lane and step.  A row with an infinity or NaN gets scale NaN and q = 0, so
-// that the projection of that row is NaN.
-template <typename T_>
+// Four values to four bytes.
+__device__ __forceinline__ uint32_t quant_pack(float a, float b, float c, float d, float s, float inv) {
+  const int x = quant_round(a, s, inv), y = quant_round(b, s, inv), z = quant_round(c, s, inv), w = quant_round(d, s, inv);
+  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+}
+
+constexpr int kQuantHeld = 8;   // 16-byte vectors of a row that a thread holds between its two passes
+
+// G threads per row (a warp, or a block where there are few rows), 16-byte loads.  The first kQuantHeld vectors of a
+// thread stay in registers, so that a row of up to G * 128 bytes is read once; the rest is read again (from L2).  A row
+// with an infinity or NaN gets scale NaN and q = 0, so that the projection of that row is NaN.
+template <typename T_, int G>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const T_* __restrict__ x, long long ldx, long long M, int K,
                                                             int8_t* __restrict__ q, long long ldq,
                                                             float* __restrict__ scale) {
-  const int lane = threadIdx.x & 31;
-  const long long warps = (long long)gridDim.x * (blockDim.x >> 5);
-  for (long long r = (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); r < M; r += warps) {
+  constexpr int V = 16 / sizeof(T_);
+  __shared__ unsigned s_mx[8];
+  const int t = threadIdx.x % G, lane = threadIdx.x & 31;
+  const int nv = K / V;   // whole vectors; the rest of the row goes value by value
+  const long long per = blockDim.x / G;
+  for (long long r = blockIdx.x * per + threadIdx.x / G; r < M; r += gridDim.x * per) {
     const T_* xr = x + r * ldx;
+    int8_t* qr = q + r * ldq;
+    uint4 h[kQuantHeld];
     unsigned mx = 0;   // |x| as bits: ordered like the values, NaN above infinity
-    for (int c = lane; c < K; c += 32) mx = max(mx, __float_as_uint(to_f32(xr[c])) & 0x7fffffffu);
+    auto take = [&](const uint4& u) {
+      if constexpr (sizeof(T_) == 2) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = max(mx, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
+      } else {
+        mx = max(mx, max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu)));
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < kQuantHeld; ++j)
+      if (t + j * G < nv) h[j] = __ldg(reinterpret_cast<const uint4*>(xr) + t + j * G);
+#pragma unroll
+    for (int j = 0; j < kQuantHeld; ++j)
+      if (t + j * G < nv) take(h[j]);
+    for (int j = t + kQuantHeld * G; j < nv; j += G) take(__ldg(reinterpret_cast<const uint4*>(xr) + j));
+    for (int c = nv * V + t; c < K; c += G) mx = max(mx, __float_as_uint(to_f32(xr[c])) & 0x7fffffffu);
     mx = __reduce_max_sync(0xffffffffu, mx);
+    if constexpr (G > 32) {
+      __syncthreads();   // the row before is done with s_mx
+      if (lane == 0) s_mx[threadIdx.x >> 5] = mx;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < G / 32; ++w) mx = max(mx, s_mx[w]);
+    }
     const bool bad = mx >= 0x7f800000u;
     const float s = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(mx) / 127.f;
-    const float inv = 1.f / s;
-    for (int c = lane; c < K; c += 32) {
-      const float v = to_f32(xr[c]);
-      q[r * ldq + c] = static_cast<int8_t>(bad ? 0 : s < kQuantTiny ? quant_round_tiny(v, s) : quant_round(v, s, inv));
+    if (t == 0) scale[r] = s;
+    if (bad || s < kQuantTiny) {   // rare
+      for (int c = t; c < K; c += G) qr[c] = static_cast<int8_t>(bad ? 0 : quant_round_tiny(to_f32(xr[c]), s));
+      continue;
     }
-    if (lane == 0) scale[r] = s;
+    const float inv = 1.f / s;
+    auto put = [&](int j, const uint4& u) {
+      if constexpr (sizeof(T_) == 2) {
+        const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z), d = unpack_bf16x2(u.w);
+        reinterpret_cast<uint2*>(qr)[j] =
+            make_uint2(quant_pack(a.x, a.y, b.x, b.y, s, inv), quant_pack(c.x, c.y, d.x, d.y, s, inv));
+      } else {
+        reinterpret_cast<uint32_t*>(qr)[j] = quant_pack(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
+                                                        __uint_as_float(u.w), s, inv);
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < kQuantHeld; ++j)
+      if (t + j * G < nv) put(t + j * G, h[j]);
+    for (int j = t + kQuantHeld * G; j < nv; j += G) put(j, __ldg(reinterpret_cast<const uint4*>(xr) + j));
+    for (int c = nv * V + t; c < K; c += G) qr[c] = static_cast<int8_t>(quant_round(to_f32(xr[c]), s, inv));
   }
+}
+
+// ---------------------------------------------------------------------------------------------------
+// Few rows (M <= 8): the weights' bytes bound it.  One warp per kFewCols output channels and all M rows; a lane takes
+// 16 bytes of K per step (dp4a), the warp adds the lanes' sums at the end.  The rows of A come from L1.
+// ---------------------------------------------------------------------------------------------------
+constexpr int kFewRows = 8, kFewCols = 4;
+
+template <typename T_, int MR>
+__global__ void __launch_bounds__(128) gemm_int8_few_kernel(const int8_t* __restrict__ A, long long lda,
+                                                            const float* __restrict__ a_scale, int M, int K,
+                                                            const int8_t* __restrict__ W, long long ldw,
+                                                            const float* __restrict__ w_scale, int N,
+                                                            const float* __restrict__ bias, T_* __restrict__ C,
+                                                            long long ldc) {
+  const int lane = threadIdx.x & 31;
+  const int n0 = (blockIdx.x * 4 + (threadIdx.x >> 5)) * kFewCols;
+  if (n0 >= N) return;
+  int acc[MR][kFewCols];
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int c = 0; c < kFewCols; ++c) acc[m][c] = 0;
+  const int nv = K / 16;
+#pragma unroll 4
+  for (int v = lane; v < nv; v += 32) {
+    int4 w[kFewCols];
+#pragma unroll
+    for (int c = 0; c < kFewCols; ++c)   // a column behind N repeats the last one
+      w[c] = __ldg(reinterpret_cast<const int4*>(W + static_cast<long long>(min(n0 + c, N - 1)) * ldw) + v);
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+      if (m < M) {
+        const int4 a = __ldg(reinterpret_cast<const int4*>(A + m * lda) + v);
+#pragma unroll
+        for (int c = 0; c < kFewCols; ++c)
+          acc[m][c] = __dp4a(a.x, w[c].x, __dp4a(a.y, w[c].y, __dp4a(a.z, w[c].z, __dp4a(a.w, w[c].w, acc[m][c]))));
+      }
+  }
+  for (int k = nv * 16 + lane; k < K; k += 32)
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+      if (m < M)
+#pragma unroll
+        for (int c = 0; c < kFewCols; ++c)
+          acc[m][c] += static_cast<int>(A[m * lda + k]) * W[static_cast<long long>(min(n0 + c, N - 1)) * ldw + k];
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+    if (m < M)
+#pragma unroll
+      for (int c = 0; c < kFewCols; ++c) {
+        const int sum = __reduce_add_sync(0xffffffffu, acc[m][c]);
+        const int n = n0 + c;
+        if (lane == c && n < N) {
+          const float v = static_cast<float>(sum) * __ldg(a_scale + m) * __ldg(w_scale + n);
+          C[m * ldc + n] = from_f32<T_>(bias != nullptr ? v + __ldg(bias + n) : v);
+        }
+      }
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -95,6 +205,12 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, ui
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
 }
+
+// Values 4q .. 4q + 3 of a slice's column scales (16-byte aligned: tiles and slices start at multiples of 32 columns).
+__device__ __forceinline__ float4 int8_scale4(const float* s, int q) { return __ldg(reinterpret_cast<const float4*>(s) + q); }
+// Chunk swizzle of the transpose buffers: rows of 4 chunks pair up in 128 bytes, rows of 8 fill them.
+template <int CH>
+__device__ __forceinline__ int int8_swz(int row) { return CH == 4 ? (row >> 1) & 3 : row & 7; }
 
 template <typename T_>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
@@ -190,34 +306,90 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       }
     }
   } else {
+    // epilogue warps 2..9 -> TMEM lane quadrants 2, 3, 0, 1, 2, 3, 0, 1; warps 2..5 take the even 32-column slices of a
+    // tile, warps 6..9 the odd ones.  A slice of 32 rows passes through a transpose buffer, so that the stores write
+    // whole row segments.
     const int quad = warp & 3;
     const int chalf = (warp - 2) >> 2;
+    constexpr int CH = 32 * sizeof(T_) / 16;   // 16-byte chunks of a row's slice
+    uint4* stg = reinterpret_cast<uint4*>(smem + p.stages * stage_bytes + 256) + (warp - 2) * 32 * CH;
     int it = 0;
     for (int tile = pair; tile < p.num_tiles; tile += npairs, ++it) {
       const int mb = tile / p.num_n_tiles, nb = tile % p.num_n_tiles;
       const int acc = it & 1;
       const uint32_t acc_par = (it >> 1) & 1;
+      const int row0 = mb * 256 + rank * 128 + quad * 32;
+      const float as = row0 + lane < p.M ? __ldg(p.a_scale + row0 + lane) : 0.f;
+      const int cols = min(p.bn, p.N - nb * p.bn);
       if (!mbar_wait(&tfull[acc], acc_par)) break;
       tc_fence_after();
-      const int row = mb * 256 + rank * 128 + quad * 32 + lane;
-      const bool row_ok = row < p.M;
-      const float as = row_ok ? __ldg(p.a_scale + row) : 0.f;
-      T_* crow = static_cast<T_*>(p.C) + (long long)row * p.ldc;
-      const int cols = min(p.bn, p.N - nb * p.bn);
       for (int c0 = chalf * 32; c0 < cols; c0 += 64) {
+        const int col0 = nb * p.bn + c0, left = min(32, cols - c0);   // the same for the whole warp
         uint32_t r[32];
         tmem_ld32(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + c0, r);
-        tmem_wait_ld();
-        if (row_ok) {
+        float v[32];
+        if (left == 32) {
+          float4 ws[8];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int col = nb * p.bn + c0 + j;
-            if (c0 + j < cols) {
-              float v = static_cast<float>(static_cast<int>(r[j])) * as * __ldg(p.w_scale + col);
-              if (p.bias != nullptr) v += __ldg(p.bias + col);
-              crow[col] = from_f32<T_>(v);
+          for (int q = 0; q < 8; ++q) ws[q] = int8_scale4(p.w_scale + col0, q);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            v[4 * q] = static_cast<float>(static_cast<int>(r[4 * q])) * as * ws[q].x;
+            v[4 * q + 1] = static_cast<float>(static_cast<int>(r[4 * q + 1])) * as * ws[q].y;
+            v[4 * q + 2] = static_cast<float>(static_cast<int>(r[4 * q + 2])) * as * ws[q].z;
+            v[4 * q + 3] = static_cast<float>(static_cast<int>(r[4 * q + 3])) * as * ws[q].w;
+          }
+          if (p.bias != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              const float4 bq = int8_scale4(p.bias + col0, q);
+              v[4 * q] += bq.x;
+              v[4 * q + 1] += bq.y;
+              v[4 * q + 2] += bq.z;
+              v[4 * q + 3] += bq.w;
             }
           }
+        } else {
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const int col = col0 + min(j, left - 1);
+            v[j] = static_cast<float>(static_cast<int>(r[j])) * as * __ldg(p.w_scale + col);
+            if (p.bias != nullptr) v[j] += __ldg(p.bias + col);
+          }
+        }
+        // row `lane`, chunk q at q ^ (a function of the row): conflict-free both ways
+#pragma unroll
+        for (int q = 0; q < CH; ++q) {
+          uint4 pk;
+          if constexpr (sizeof(T_) == 2) {
+            pk.x = pack_bf16x2(v[q * 8 + 0], v[q * 8 + 1]);
+            pk.y = pack_bf16x2(v[q * 8 + 2], v[q * 8 + 3]);
+            pk.z = pack_bf16x2(v[q * 8 + 4], v[q * 8 + 5]);
+            pk.w = pack_bf16x2(v[q * 8 + 6], v[q * 8 + 7]);
+          } else {
+            pk = make_uint4(__float_as_uint(v[q * 4]), __float_as_uint(v[q * 4 + 1]), __float_as_uint(v[q * 4 + 2]),
+                            __float_as_uint(v[q * 4 + 3]));
+          }
+          stg[lane * CH + (q ^ int8_swz<CH>(lane))] = pk;
+        }
+        __syncwarp();
+        if (p.vec && left == 32) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int rr = (i * 32 + lane) / CH, q = lane % CH;
+            if (row0 + rr < p.M)
+              reinterpret_cast<uint4*>(static_cast<T_*>(p.C) + (row0 + rr) * p.ldc + col0)[q] =
+                  stg[rr * CH + (q ^ int8_swz<CH>(rr))];
+          }
+        } else {   // rows of C that do not start on 16 bytes, and the last columns: lane = column
+          constexpr int E = 16 / sizeof(T_);
+          const int rows = min(32, p.M - row0);
+          for (int rr = 0; rr < rows; ++rr)
+            if (lane < left)
+              (static_cast<T_*>(p.C) + (row0 + rr) * p.ldc + col0)[lane] =
+                  reinterpret_cast<const T_*>(stg + rr * CH + ((lane / E) ^ int8_swz<CH>(rr)))[lane % E];
         }
         __syncwarp();
       }

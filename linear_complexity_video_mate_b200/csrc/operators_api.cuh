@@ -369,6 +369,31 @@ bool make_tmap_s8(CUtensorMap* m, const void* ptr, long long rows, long long col
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A warp per row where there are enough rows to fill the SMs, else a block per row.
+template <typename T_>
+void launch_quantize(const T_* x, long long ldx, long long M, int K, void* q, long long ldq, float* scale,
+                     cudaStream_t st) {
+  int8_t* q8 = static_cast<int8_t*>(q);
+  const long long sms = device_sms();
+  if (M >= 16 * sms)
+    quantize_rows_kernel<T_, 32>
+        <<<static_cast<int>(std::min<long long>((M + 7) / 8, 8 * sms)), 256, 0, st>>>(x, ldx, M, K, q8, ldq, scale);
+  else
+    quantize_rows_kernel<T_, 256>
+        <<<static_cast<int>(std::min<long long>(M, 8 * sms)), 256, 0, st>>>(x, ldx, M, K, q8, ldq, scale);
+}
+
+template <typename T_>
+void launch_int8_few(const int8_t* A, long long lda, const float* a_scale, int M, int K, const int8_t* W, long long ldw,
+                     const float* w_scale, int N, const float* bias, void* C, long long ldc, cudaStream_t st) {
+  T_* c = static_cast<T_*>(C);
+  const int blocks = ceil_div(N, 4 * kFewCols);
+  auto kernel = M == 1 ? gemm_int8_few_kernel<T_, 1>
+                       : M == 2 ? gemm_int8_few_kernel<T_, 2>
+                                : M <= 4 ? gemm_int8_few_kernel<T_, 4> : gemm_int8_few_kernel<T_, kFewRows>;
+  kernel<<<blocks, 128, 0, st>>>(A, lda, a_scale, M, K, W, ldw, w_scale, N, bias, c, ldc);
+}
+
 }  // namespace
 
 extern "C" {
@@ -384,14 +409,9 @@ mate_status mate_quantize_rows(const void* x, long long ldx, long long M, int K,
   t_launches = 0;
   if (M == 0) return MATE_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int blocks = static_cast<int>(std::min<long long>((M + 7) / 8, (long long)device_sms() * 8));
   trace_begin(MATE_K_QUANTIZE_ROWS, st);
-  if (dtype == MATE_BF16)
-    quantize_rows_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(static_cast<const __nv_bfloat16*>(x), ldx, M, K,
-                                                                static_cast<int8_t*>(q), ldq, scale);
-  else
-    quantize_rows_kernel<float><<<blocks, 256, 0, st>>>(static_cast<const float*>(x), ldx, M, K,
-                                                        static_cast<int8_t*>(q), ldq, scale);
+  if (dtype == MATE_BF16) launch_quantize(static_cast<const __nv_bfloat16*>(x), ldx, M, K, q, ldq, scale, st);
+  else launch_quantize(static_cast<const float*>(x), ldx, M, K, q, ldq, scale, st);
   MATE_LAUNCH_CHECK();
   return MATE_OK;
 }
@@ -410,11 +430,24 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   t_launches = 0;
   if (M == 0) return MATE_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (M <= kFewRows) {
+    const int8_t *a = static_cast<const int8_t*>(A), *w = static_cast<const int8_t*>(Wt);
+    trace_begin(MATE_K_PROJECT_INT8, st);
+    if (out_dtype == MATE_BF16)
+      launch_int8_few<__nv_bfloat16>(a, lda, a_scale, static_cast<int>(M), K, w, ldw, w_scale, N, bias, C, ldc, st);
+    else
+      launch_int8_few<float>(a, lda, a_scale, static_cast<int>(M), K, w, ldw, w_scale, N, bias, C, ldc, st);
+    MATE_LAUNCH_CHECK();
+    return MATE_OK;
+  }
   Int8GemmParams p;
   p.M = static_cast<int>(M);
   p.N = N;
   p.K = K;
-  p.bn = N >= 256 ? 256 : (N + 31) / 32 * 32;
+  // the widest tile that still gives every pair of SMs one
+  const int pairs_all = device_sms() / 2;
+  p.bn = 256;
+  while (p.bn > 32 && (p.bn / 2 >= N || (long long)ceil_div(M, 256) * ceil_div(N, p.bn) < pairs_all)) p.bn /= 2;
   p.num_n_tiles = ceil_div(N, p.bn);
   const long long tiles = (long long)ceil_div(M, 256) * p.num_n_tiles;
   if (tiles >= (1LL << 31)) return MATE_ERR_SHAPE;
@@ -426,13 +459,14 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   p.ldc = ldc;
   p.vec = ldc * (out_dtype == MATE_BF16 ? 2 : 4) % 16 == 0;
   const uint32_t sb = int8_stage_bytes(p.bn);
-  p.stages = std::min<int>(8, static_cast<int>((kSmemLimit - 1024 - 256) / sb));
+  const uint32_t stage_out = kI8EpiWarps * 32 * 32 * (out_dtype == MATE_BF16 ? 2 : 4);   // the transpose buffers
+  p.stages = std::min<int>(8, static_cast<int>((kSmemLimit - 1024 - 256 - stage_out) / sb));
   CUtensorMap ta, tb;
   if (!make_tmap_s8(&ta, A, M, K, lda, 128) || !make_tmap_s8(&tb, Wt, N, K, ldw, p.bn / 2)) return MATE_ERR_CUDA;
-  const size_t smem = 1024 + (size_t)p.stages * sb + 256;
+  const size_t smem = 1024 + (size_t)p.stages * sb + 256 + stage_out;
   auto kernel = out_dtype == MATE_BF16 ? gemm_int8_pair_kernel<__nv_bfloat16> : gemm_int8_pair_kernel<float>;
   if (!set_smem(kernel, smem)) return MATE_ERR_CUDA;
-  const int pairs = std::min(p.num_tiles, device_sms() / 2);
+  const int pairs = std::min(p.num_tiles, pairs_all);
   trace_begin(MATE_K_PROJECT_INT8, st);
   kernel<<<2 * pairs, kI8Threads, smem, st>>>(ta, tb, p);
   MATE_LAUNCH_CHECK();
