@@ -69,29 +69,6 @@ __device__ __forceinline__ int gs_row(const GatedScanParams& p, int s) {
   return scan_to_raster(p.reverse ? p.n - 1 - s : s, p.T, p.H, p.W, p.order);
 }
 
-// Pairs of fp32 values in one instruction each (round to nearest, as the scalar forms).
-__device__ __forceinline__ unsigned long long gs_u64(float2 a) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-  return r;
-}
-__device__ __forceinline__ float2 gs_f2(unsigned long long v) {
-  float2 d;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  unsigned long long d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(gs_u64(a)), "l"(gs_u64(b)), "l"(gs_u64(c)));
-  return gs_f2(d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  unsigned long long d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(gs_u64(a)), "l"(gs_u64(b)));
-  return gs_f2(d);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
 // a = sigmoid(z) and 1 - a, each to full precision, from t = -z log2 e: with e = 2^t, a = 1 / (1 + e) (0 where that is
 // below the normal numbers), and 1 - a is e a where a is above 1/2, the difference where it is not (there e a may be
 // infinity times 0).  NaN stays NaN.
@@ -111,7 +88,7 @@ constexpr float kGsLog2e = -1.4426950408889634f;
 struct GsPair {
   unsigned long long x, y;   // of a thread's two channels
 };
-__device__ __forceinline__ unsigned long long gs_word(float lo, float hi) { return gs_u64(make_float2(lo, hi)); }
+__device__ __forceinline__ unsigned long long gs_word(float lo, float hi) { return f2_bits(make_float2(lo, hi)); }
 __device__ __forceinline__ void gs_publish(unsigned long long* w, float2 A, float2 H) {
   // the low word may not look empty: a NaN gets the payload that arithmetic gives it
   if (A.x != A.x) A.x = __uint_as_float(0x7fffffffu);
@@ -311,7 +288,7 @@ __device__ __forceinline__ bool gs_before(const GatedScanParams& p, GsSmem<T_, N
         const unsigned long long* wg = p.group + (k / kGsGroup) * step + at;
         GsPair g = gs_look(wg);
         ok = gs_wait(p, wg, &g);
-        start = make_float2(gs_f2(g.x).y, gs_f2(g.y).y);
+        start = make_float2(f2_from(g.x).y, f2_from(g.y).y);
       }
       sm.lg[lane] = start;
     }
@@ -319,7 +296,7 @@ __device__ __forceinline__ bool gs_before(const GatedScanParams& p, GsSmem<T_, N
     for (int j = 0; j < per; ++j)
       if (j0 + j < m && ok) {
         ok = gs_wait(p, w + j * step, &v[j]);
-        const float2 u = gs_f2(v[j].x), q = gs_f2(v[j].y);
+        const float2 u = f2_from(v[j].x), q = f2_from(v[j].y);
         H = fma2(make_float2(u.x, q.x), H, make_float2(u.y, q.y));
         A = mul_f32x2(A, make_float2(u.x, q.x));
       }

@@ -12,18 +12,24 @@ namespace mate {
 // Rows to int8: scale = max|x| / 127 (fp32), q = x / scale to the nearest integer, ties to even.
 // ---------------------------------------------------------------------------------------------------
 
-// x / s to the nearest integer for |x| <= 127.5 s, decided exactly: the product with 1/s is off by at most
-// 127 * 2^-23 < 2^-10, so only quotients that near a midpoint need the remainder x - k s, which one fma gives
-// without error there (it has at most as many bits as x).
-__device__ __forceinline__ int quant_round(float x, float s, float inv) {
+// x / s to the nearest integer k for |x| <= 127.5 s: t = x (1/s) is off by at most 127 * 2^-23 < 2^-15, so rounding t
+// (by adding 1.5 * 2^23, which leaves k in the sum's low byte) is right unless t is within 2^-15 of a midpoint.
+__device__ __forceinline__ float quant_near(float x, float inv, uint32_t* k) {
   const float t = x * inv;
-  float k = rintf(t);
-  if (fabsf(t - k) > 0.4990234375f) {
-    const float e2 = 2.f * fmaf(-k, s, x);
-    if (e2 > s || (e2 == s && (static_cast<int>(k) & 1))) k += 1.f;
-    else if (e2 < -s || (e2 == -s && (static_cast<int>(k) & 1))) k -= 1.f;
-  }
-  return static_cast<int>(k);
+  const float m = t + 12582912.f;
+  *k = __float_as_uint(m);
+  return fabsf(t - (m - 12582912.f));   // distance from the integer taken
+}
+constexpr float kQuantMid = 0.5f - 1.f / 32768;
+
+// The same, decided exactly: the remainder x - k s, which one fma gives without error next to a midpoint (it has at most
+// as many bits as x there), ties to even.
+__device__ __forceinline__ uint32_t quant_round(float x, float s, float inv) {
+  float k = rintf(x * inv);
+  const float e2 = 2.f * fmaf(-k, s, x);
+  if (e2 > s || (e2 == s && (static_cast<int>(k) & 1))) k += 1.f;
+  else if (e2 < -s || (e2 == -s && (static_cast<int>(k) & 1))) k -= 1.f;
+  return static_cast<uint32_t>(static_cast<int>(k));
 }
 
 constexpr float kQuantTiny = 1e-30f;   // scales below: 1 / s may overflow, the quotient is formed in 64 bits
@@ -35,7 +41,15 @@ __device__ __forceinline__ int quant_round_tiny(float x, float s) {
 
 // Four values to four bytes.
 __device__ __forceinline__ uint32_t quant_pack(float a, float b, float c, float d, float s, float inv) {
-  const int x = quant_round(a, s, inv), y = quant_round(b, s, inv), z = quant_round(c, s, inv), w = quant_round(d, s, inv);
+  uint32_t x, y, z, w;
+  const float off = fmaxf(fmaxf(quant_near(a, inv, &x), quant_near(b, inv, &y)),
+                          fmaxf(quant_near(c, inv, &z), quant_near(d, inv, &w)));
+  if (off > kQuantMid) {
+    x = quant_round(a, s, inv);
+    y = quant_round(b, s, inv);
+    z = quant_round(c, s, inv);
+    w = quant_round(d, s, inv);
+  }
   return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
 }
 
@@ -45,7 +59,7 @@ constexpr int kQuantHeld = 8;   // 16-byte vectors of a row that a thread holds 
 // thread stay in registers, so that a row of up to G * 128 bytes is read once; the rest is read again (from L2).  A row
 // with an infinity or NaN gets scale NaN and q = 0, so that the projection of that row is NaN.
 template <typename T_, int G>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const T_* __restrict__ x, long long ldx, long long M, int K,
+__global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const T_* __restrict__ x, long long ldx, long long M, int K,
                                                             int8_t* __restrict__ q, long long ldq,
                                                             float* __restrict__ scale) {
   constexpr int V = 16 / sizeof(T_);
@@ -57,15 +71,13 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T_* __restrict
     const T_* xr = x + r * ldx;
     int8_t* qr = q + r * ldq;
     uint4 h[kQuantHeld];
-    unsigned mx = 0;   // |x| as bits: ordered like the values, NaN above infinity
+    unsigned mx = 0;   // |x| as bits: ordered like the values, NaN above infinity (bf16: two 16-bit halves, joined below)
     auto take = [&](const uint4& u) {
-      if constexpr (sizeof(T_) == 2) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx = max(mx, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
-      } else {
+      if constexpr (sizeof(T_) == 2)
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                   __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+      else
         mx = max(mx, max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu)));
-      }
     };
 #pragma unroll
     for (int j = 0; j < kQuantHeld; ++j)
@@ -74,6 +86,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T_* __restrict
     for (int j = 0; j < kQuantHeld; ++j)
       if (t + j * G < nv) take(h[j]);
     for (int j = t + kQuantHeld * G; j < nv; j += G) take(__ldg(reinterpret_cast<const uint4*>(xr) + j));
+    if constexpr (sizeof(T_) == 2) mx = max(mx << 16, mx & 0xffff0000u);
     for (int c = nv * V + t; c < K; c += G) mx = max(mx, __float_as_uint(to_f32(xr[c])) & 0x7fffffffu);
     mx = __reduce_max_sync(0xffffffffu, mx);
     if constexpr (G > 32) {
@@ -206,8 +219,6 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// Values 4q .. 4q + 3 of a slice's column scales (16-byte aligned: tiles and slices start at multiples of 32 columns).
-__device__ __forceinline__ float4 int8_scale4(const float* s, int q) { return __ldg(reinterpret_cast<const float4*>(s) + q); }
 // Chunk swizzle of the transpose buffers: rows of 4 chunks pair up in 128 bytes, rows of 8 fill them.
 template <int CH>
 __device__ __forceinline__ int int8_swz(int row) { return CH == 4 ? (row >> 1) & 3 : row & 7; }
@@ -223,7 +234,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
   uint64_t* full = bars;                  // leader only: operands of both CTAs landed
   uint64_t* empty = bars + p.stages;      // both CTAs: the pair MMAs are done with this stage
   uint64_t* tfull = bars + 2 * p.stages;  // both CTAs: accumulator ready
-  uint64_t* tempty = tfull + 2;           // leader only: both CTAs' epilogues drained the accumulator
+  uint64_t* tempty = tfull + 2;           // the CTA's epilogue drained the accumulator (leader: and the other CTA's)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
 
   const int warp = threadIdx.x >> 5;
@@ -240,7 +251,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * kI8EpiWarps);
+      mbar_init(&tempty[a], kI8EpiWarps + (leader ? 1 : 0));
     }
     mbar_fence_init();
     prefetch_tensormap(&tmA);
@@ -304,6 +315,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         mma_commit_pair(map_to_cta(&tfull[acc], 0));
         mma_commit_pair(map_to_cta(&tfull[acc], 1));
       }
+    } else if (lane == 0) {
+      // passes the other CTA's drained accumulators on: an arrival on the leader's barrier by the epilogue warps
+      // themselves would wait for their stores to reach memory first
+      int it = 0;
+      for (int tile = pair; tile < p.num_tiles; tile += npairs, ++it) {
+        if (!mbar_wait(&tempty[it & 1], (it >> 1) & 1)) break;
+        mbar_arrive_cluster(map_to_cta(&tempty[it & 1], 0));
+      }
     }
   } else {
     // epilogue warps 2..9 -> TMEM lane quadrants 2, 3, 0, 1, 2, 3, 0, 1; warps 2..5 take the even 32-column slices of a
@@ -313,6 +332,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
     const int chalf = (warp - 2) >> 2;
     constexpr int CH = 32 * sizeof(T_) / 16;   // 16-byte chunks of a row's slice
     uint4* stg = reinterpret_cast<uint4*>(smem + p.stages * stage_bytes + 256) + (warp - 2) * 32 * CH;
+    // the column scales and biases of the warp's slices, [4][32] each, fetched while the accumulator fills
+    float* sc = reinterpret_cast<float*>(smem + p.stages * stage_bytes + 256 + kI8EpiWarps * 512 * CH) + (warp - 2) * 256;
+    const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + chalf * 32;
     int it = 0;
     for (int tile = pair; tile < p.num_tiles; tile += npairs, ++it) {
       const int mb = tile / p.num_n_tiles, nb = tile % p.num_n_tiles;
@@ -320,68 +342,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       const uint32_t acc_par = (it >> 1) & 1;
       const int row0 = mb * 256 + rank * 128 + quad * 32;
       const float as = row0 + lane < p.M ? __ldg(p.a_scale + row0 + lane) : 0.f;
-      const int cols = min(p.bn, p.N - nb * p.bn);
+      const int cols = min(p.bn, p.N - nb * p.bn) - chalf * 32;   // of the tile, from this warp's first slice on
+      const int first = nb * p.bn + chalf * 32;
+      // this lane's chunk of the first 32 / CH rows of a slice, and how far the next rows are
+      T_* c_lane = static_cast<T_*>(p.C) + (row0 + lane / CH) * p.ldc + (lane % CH) * (16 / sizeof(T_));
+      const long long step = p.ldc * static_cast<long long>(sizeof(T_)) / 16 * (32 / CH);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = i * 64 + lane;
+        sc[i * 32 + lane] = c < cols ? __ldg(p.w_scale + first + c) : 0.f;
+        sc[128 + i * 32 + lane] = c < cols && p.bias != nullptr ? __ldg(p.bias + first + c) : 0.f;
+      }
+      __syncwarp();
       if (!mbar_wait(&tfull[acc], acc_par)) break;
       tc_fence_after();
-      for (int c0 = chalf * 32; c0 < cols; c0 += 64) {
-        const int col0 = nb * p.bn + c0, left = min(32, cols - c0);   // the same for the whole warp
-        uint32_t r[32];
-        tmem_ld32(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256 + c0, r);
-        float v[32];
-        if (left == 32) {
-          float4 ws[8];
+      uint32_t r[32];
+      if (cols > 0) {
+        tmem_ld32(t_lane + acc * 256, r);
+        tmem_wait_ld();
+      }
+      for (int i = 0; i * 64 < cols; ++i) {
+        const int col0 = first + i * 64, left = min(32, cols - i * 64);   // the same for the whole warp
+        float2 v[16];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) ws[q] = int8_scale4(p.w_scale + col0, q);
-          tmem_wait_ld();
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            v[4 * q] = static_cast<float>(static_cast<int>(r[4 * q])) * as * ws[q].x;
-            v[4 * q + 1] = static_cast<float>(static_cast<int>(r[4 * q + 1])) * as * ws[q].y;
-            v[4 * q + 2] = static_cast<float>(static_cast<int>(r[4 * q + 2])) * as * ws[q].z;
-            v[4 * q + 3] = static_cast<float>(static_cast<int>(r[4 * q + 3])) * as * ws[q].w;
-          }
-          if (p.bias != nullptr) {
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              const float4 bq = int8_scale4(p.bias + col0, q);
-              v[4 * q] += bq.x;
-              v[4 * q + 1] += bq.y;
-              v[4 * q + 2] += bq.z;
-              v[4 * q + 3] += bq.w;
-            }
-          }
-        } else {
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const int col = col0 + min(j, left - 1);
-            v[j] = static_cast<float>(static_cast<int>(r[j])) * as * __ldg(p.w_scale + col);
-            if (p.bias != nullptr) v[j] += __ldg(p.bias + col);
-          }
+        for (int q = 0; q < 8; ++q) {   // (acc a_scale) w_scale + bias
+          const float4 ws = reinterpret_cast<const float4*>(sc + i * 32)[q];
+          const float4 bq = reinterpret_cast<const float4*>(sc + 128 + i * 32)[q];
+          const float2 lo = make_float2(static_cast<int>(r[4 * q]), static_cast<int>(r[4 * q + 1]));
+          const float2 hi = make_float2(static_cast<int>(r[4 * q + 2]), static_cast<int>(r[4 * q + 3]));
+          v[2 * q] = fma2(mul_f32x2(lo, both(as)), make_float2(ws.x, ws.y), make_float2(bq.x, bq.y));
+          v[2 * q + 1] = fma2(mul_f32x2(hi, both(as)), make_float2(ws.z, ws.w), make_float2(bq.z, bq.w));
+        }
+        const bool more = (i + 1) * 64 < cols;
+        if (more) {
+          tmem_ld32(t_lane + acc * 256 + (i + 1) * 64, r);   // the next slice, while this one is stored
+        } else {   // the last one is in registers: the accumulator is free
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc]);
         }
         // row `lane`, chunk q at q ^ (a function of the row): conflict-free both ways
 #pragma unroll
         for (int q = 0; q < CH; ++q) {
           uint4 pk;
-          if constexpr (sizeof(T_) == 2) {
-            pk.x = pack_bf16x2(v[q * 8 + 0], v[q * 8 + 1]);
-            pk.y = pack_bf16x2(v[q * 8 + 2], v[q * 8 + 3]);
-            pk.z = pack_bf16x2(v[q * 8 + 4], v[q * 8 + 5]);
-            pk.w = pack_bf16x2(v[q * 8 + 6], v[q * 8 + 7]);
-          } else {
-            pk = make_uint4(__float_as_uint(v[q * 4]), __float_as_uint(v[q * 4 + 1]), __float_as_uint(v[q * 4 + 2]),
-                            __float_as_uint(v[q * 4 + 3]));
-          }
+          if constexpr (sizeof(T_) == 2)
+            pk = make_uint4(pack_bf16x2(v[q * 4].x, v[q * 4].y), pack_bf16x2(v[q * 4 + 1].x, v[q * 4 + 1].y),
+                            pack_bf16x2(v[q * 4 + 2].x, v[q * 4 + 2].y), pack_bf16x2(v[q * 4 + 3].x, v[q * 4 + 3].y));
+          else
+            pk = make_uint4(__float_as_uint(v[q * 2].x), __float_as_uint(v[q * 2].y), __float_as_uint(v[q * 2 + 1].x),
+                            __float_as_uint(v[q * 2 + 1].y));
           stg[lane * CH + (q ^ int8_swz<CH>(lane))] = pk;
         }
         __syncwarp();
         if (p.vec && left == 32) {
+          uint4* dst = reinterpret_cast<uint4*>(c_lane + col0);
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const int rr = (i * 32 + lane) / CH, q = lane % CH;
-            if (row0 + rr < p.M)
-              reinterpret_cast<uint4*>(static_cast<T_*>(p.C) + (row0 + rr) * p.ldc + col0)[q] =
-                  stg[rr * CH + (q ^ int8_swz<CH>(rr))];
+          for (int j = 0; j < CH; ++j, dst += step) {
+            const int rr = j * (32 / CH) + lane / CH;
+            if (row0 + rr < p.M) *dst = stg[rr * CH + ((lane % CH) ^ int8_swz<CH>(rr))];
           }
         } else {   // rows of C that do not start on 16 bytes, and the last columns: lane = column
           constexpr int E = 16 / sizeof(T_);
@@ -391,11 +409,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
               (static_cast<T_*>(p.C) + (row0 + rr) * p.ldc + col0)[lane] =
                   reinterpret_cast<const T_*>(stg + rr * CH + ((lane / E) ^ int8_swz<CH>(rr)))[lane % E];
         }
+        if (more) tmem_wait_ld();
         __syncwarp();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(map_to_cta(&tempty[acc], 0));
+      if (cols <= 0) {   // a narrow last tile has no slice for these warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[acc]);
+      }
     }
   }
   tc_fence_before();

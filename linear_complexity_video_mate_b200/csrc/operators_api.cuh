@@ -459,7 +459,8 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   p.ldc = ldc;
   p.vec = ldc * (out_dtype == MATE_BF16 ? 2 : 4) % 16 == 0;
   const uint32_t sb = int8_stage_bytes(p.bn);
-  const uint32_t stage_out = kI8EpiWarps * 32 * 32 * (out_dtype == MATE_BF16 ? 2 : 4);   // the transpose buffers
+  // the epilogue's transpose buffers, scales and biases
+  const uint32_t stage_out = kI8EpiWarps * (32 * 32 * (out_dtype == MATE_BF16 ? 2 : 4) + 1024);
   p.stages = std::min<int>(8, static_cast<int>((kSmemLimit - 1024 - 256 - stage_out) / sb));
   CUtensorMap ta, tb;
   if (!make_tmap_s8(&ta, A, M, K, lda, 128) || !make_tmap_s8(&tb, Wt, N, K, ldw, p.bn / 2)) return MATE_ERR_CUDA;
