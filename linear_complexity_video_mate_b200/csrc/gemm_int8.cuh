@@ -184,25 +184,89 @@ __global__ void __launch_bounds__(128) gemm_int8_few_kernel(const int8_t* __rest
 // The product: the two-SM persistent pipeline of gemm_bf16.cuh with int8 operands (kind::i8, int32 accumulators).
 // A cluster of 2 CTAs computes a 256 x bn tile; each CTA loads its 128 rows of A and bn/2 rows of W (TMA, 128 bytes
 // of K per stage, zeros behind K), the leader issues the MMAs, two TMEM accumulators alternate.
+//
+// An MMA takes 128 cycles (256 x 256 x 32) and reads 8 KB of each CTA's shared memory meanwhile, half of what that
+// memory gives; the loads of a stage write as much again, and the epilogue stages its output there too.  So shared
+// memory is what bounds the product at short K, and both sides are kept low:
+//   KEEP: for K <= kI8KeepK a CTA's half of a column tile of W stays in shared memory while the pair walks down the
+//   rows, so that only A streams;
+//   the epilogue writes a slice of the output to shared memory once and a TMA store takes it from there.
 // ---------------------------------------------------------------------------------------------------
 struct Int8GemmParams {
   int M, N, K;
-  int bn;            // tile N (multiple of 32, <= 256)
+  int bn;              // tile N (multiple of 32, <= 256)
   int num_n_tiles, num_tiles;
   int stages;
+  int slots, groups;   // KEEP: column tiles worked on at a time, pairs per column tile
   const float* a_scale;
   const float* w_scale;
   const float* bias;   // or null
   void* C;
   long long ldc;
-  int vec;             // rows of C start on 16 bytes
+  int vec;             // rows of C start on 16 bytes: TMA stores
+};
+
+struct Int8Maps {
+  CUtensorMap a, w, c;
 };
 
 constexpr int kI8BK = 128;                               // bytes of K per stage
+constexpr int kI8KeepK = 1024;
 constexpr int kI8EpiWarps = 8;
 constexpr int kI8Threads = (2 + kI8EpiWarps) * 32;
 
-__host__ __device__ inline uint32_t int8_stage_bytes(int bn) { return 128 * 128 + (bn / 2) * 128; }
+__host__ __device__ inline uint32_t int8_stage_bytes(int bn, bool keep) {
+  return 128 * 128 + (keep ? 0 : (bn / 2) * 128);
+}
+__host__ __device__ inline uint32_t int8_kept_bytes(int bn, int K, bool keep) {
+  return keep ? (K + kI8BK - 1) / kI8BK * (bn / 2) * 128 : 0;
+}
+// Behind the ring: a 32 x 32 output slice per epilogue warp (1 KB aligned), 256 bytes of barriers, and per epilogue warp
+// the scales and biases of its four slices.
+__host__ __device__ inline uint32_t int8_out_bytes(int es) { return kI8EpiWarps * 32 * 32 * es; }
+constexpr uint32_t kI8Behind = 256 + kI8EpiWarps * 1024;
+
+// The tiles of a pair in order.  KEEP: all rows of a column tile (every groups-th), then its next column tile, so that
+// the pairs on different columns read the same rows of A at about the same time.  Else tiles pair, pair + pairs, ...
+// with the columns fastest.
+template <bool KEEP>
+struct Int8Walk {
+  int mb, nb, tile, step, mblocks;
+  __device__ __forceinline__ Int8Walk(const Int8GemmParams& p, int pair, int npairs) {
+    if constexpr (KEEP) {
+      mblocks = (p.M + 255) / 256;
+      nb = pair % p.slots;
+      mb = tile = pair / p.slots;   // its first row tile
+      step = p.groups;
+    } else {
+      tile = pair;
+      step = npairs;
+      set(p);
+    }
+  }
+  __device__ __forceinline__ void set(const Int8GemmParams& p) {
+    mb = tile / p.num_n_tiles;
+    nb = tile - mb * p.num_n_tiles;
+  }
+  __device__ __forceinline__ bool done(const Int8GemmParams& p) const {
+    if constexpr (KEEP) return nb >= p.num_n_tiles || tile >= mblocks;
+    else return tile >= p.num_tiles;
+  }
+  __device__ __forceinline__ bool column_starts() const { return KEEP && mb == tile; }
+  __device__ __forceinline__ bool column_ends() const { return KEEP && mb + step >= mblocks; }
+  __device__ __forceinline__ void next(const Int8GemmParams& p) {
+    if constexpr (KEEP) {
+      mb += step;
+      if (mb >= mblocks) {
+        mb = tile;
+        nb += p.slots;
+      }
+    } else {
+      tile += step;
+      set(p);
+    }
+  }
+};
 
 // int8 x int8 -> int32, both operands K-major.
 __host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
@@ -219,23 +283,48 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, ui
       : "memory");
 }
 
-// Chunk swizzle of the transpose buffers: rows of 4 chunks pair up in 128 bytes, rows of 8 fill them.
+// Arrives once on the barrier at this shared-memory offset in both CTAs of the pair when the pair MMAs issued so far
+// have completed.
+__device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// Tiled store from this CTA's shared memory (rows behind the matrix are left out); one thread issues it, and the source may be written again once tma_store_read() returns there.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(smem_u32(src))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Chunk swizzle of a staged slice: rows of 4 chunks (the map's 64-byte swizzle) or 8 (its 128-byte swizzle).
 template <int CH>
 __device__ __forceinline__ int int8_swz(int row) { return CH == 4 ? (row >> 1) & 3 : row & 7; }
 
-template <typename T_>
+template <typename T_, bool KEEP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
-    gemm_int8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                          const Int8GemmParams p) {
+    gemm_int8_pair_kernel(const __grid_constant__ Int8Maps maps, const Int8GemmParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t stage_bytes = int8_stage_bytes(p.bn);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.stages * stage_bytes);
+  const uint32_t stage_bytes = int8_stage_bytes(p.bn, KEEP);
+  uint8_t* kept = smem;                                  // KEEP: W rows of the column tile, 128 bytes of K per block
+  uint8_t* ring = smem + int8_kept_bytes(p.bn, p.K, KEEP);
+  uint8_t* out = ring + p.stages * stage_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(out + int8_out_bytes(sizeof(T_)));
   uint64_t* full = bars;                  // leader only: operands of both CTAs landed
   uint64_t* empty = bars + p.stages;      // both CTAs: the pair MMAs are done with this stage
   uint64_t* tfull = bars + 2 * p.stages;  // both CTAs: accumulator ready
   uint64_t* tempty = tfull + 2;           // the CTA's epilogue drained the accumulator (leader: and the other CTA's)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* kfull = tempty + 2;           // KEEP, leader only: W rows of the column tile landed
+  uint64_t* kempty = kfull + 1;           // KEEP, both CTAs: the pair MMAs are done with them
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kempty + 1);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -253,9 +342,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], kI8EpiWarps + (leader ? 1 : 0));
     }
+    mbar_init(kfull, 1);
+    mbar_init(kempty, 1);
     mbar_fence_init();
-    prefetch_tensormap(&tmA);
-    prefetch_tensormap(&tmB);
+    prefetch_tensormap(&maps.a);
+    prefetch_tensormap(&maps.w);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, 512);
@@ -268,92 +359,98 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
+      uint32_t stage = 0, phase = 0, kphase = 0;
       bool ok = true;
-      for (int tile = pair; tile < p.num_tiles && ok; tile += npairs) {
-        const int mb = tile / p.num_n_tiles, nb = tile % p.num_n_tiles;
+      for (Int8Walk<KEEP> w(p, pair, npairs); ok && !w.done(p); w.next(p)) {
         // the pair MMA takes W rows [0, n_mma/2) from each CTA (n_mma: the tile's columns rounded up to 32)
-        const int n_mma = min(p.bn, (p.N - nb * p.bn + 31) & ~31);
+        const int n_mma = min(p.bn, (p.N - w.nb * p.bn + 31) & ~31);
+        const int row_w = w.nb * p.bn + rank * (n_mma / 2);
+        if (w.column_starts()) {
+          if (!mbar_wait(kempty, kphase ^ 1)) break;
+          kphase ^= 1;
+          if (leader) mbar_arrive_expect_tx(kfull, 2 * nk * (p.bn / 2) * 128);
+          for (int kb = 0; kb < nk; ++kb)
+            tma_load_2d_pair(&maps.w, map_to_cta(kfull, 0), kept + kb * (p.bn / 2) * 128, kb * kI8BK, row_w);
+        }
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
-          uint8_t* sa = smem + stage * stage_bytes;
+          uint8_t* sa = ring + stage * stage_bytes;
           const uint32_t full_leader = map_to_cta(&full[stage], 0);
           if (leader) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);
-          tma_load_2d_pair(&tmA, full_leader, sa, kb * kI8BK, mb * 256 + rank * 128);
-          tma_load_2d_pair(&tmB, full_leader, sa + 128 * 128, kb * kI8BK, nb * p.bn + rank * (n_mma / 2));
+          tma_load_2d_pair(&maps.a, full_leader, sa, kb * kI8BK, w.mb * 256 + rank * 128);
+          if (!KEEP) tma_load_2d_pair(&maps.w, full_leader, sa + 128 * 128, kb * kI8BK, row_w);
           if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
         }
       }
     }
   } else if (warp == 1) {
     if (leader && lane == 0) {
-      uint32_t stage = 0, phase = 0;
+      uint32_t stage = 0, phase = 0, kphase = 0;
+      const uint64_t ring_desc = desc_sw128(smem_u32(ring), 16, 1024), kept_desc = desc_sw128(smem_u32(kept), 16, 1024);
       int it = 0;
       bool ok = true;
-      for (int tile = pair; tile < p.num_tiles && ok; tile += npairs, ++it) {
+      for (Int8Walk<KEEP> w(p, pair, npairs); ok && !w.done(p); w.next(p), ++it) {
         const int acc = it & 1;
         const uint32_t acc_par = (it >> 1) & 1;
-        const int nb = tile % p.num_n_tiles;
-        const int n_mma = min(p.bn, (p.N - nb * p.bn + 31) & ~31);
+        const int n_mma = min(p.bn, (p.N - w.nb * p.bn + 31) & ~31);
         const uint32_t idesc = idesc_s8_s32(256, n_mma);
+        if (w.column_starts()) {
+          if (!mbar_wait(kfull, kphase)) break;
+          kphase ^= 1;
+        }
         if (!mbar_wait(&tempty[acc], acc_par ^ 1)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
         for (int kb = 0; kb < nk; ++kb) {
           if (!mbar_wait(&full[stage], phase)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * stage_bytes);
-          const uint32_t sb = sa + 128 * 128;
+          const uint64_t da = ring_desc + stage * (stage_bytes >> 4);
+          const uint64_t db = KEEP ? kept_desc + kb * ((p.bn / 2) * 128 >> 4) : da + (128 * 128 >> 4);
 #pragma unroll
-          for (int k = 0; k < kI8BK / 32; ++k)
-            mma_i8_pair(d_tmem, desc_sw128(sa + k * 32, 16, 1024), desc_sw128(sb + k * 32, 16, 1024), idesc,
-                        (kb | k) != 0);
-          mma_commit_pair(map_to_cta(&empty[stage], 0));
-          mma_commit_pair(map_to_cta(&empty[stage], 1));
+          for (int k = 0; k < kI8BK / 32; ++k)   // 32 bytes of K further: 2 in the descriptor's 16-byte address units
+            mma_i8_pair(d_tmem, da + 2 * k, db + 2 * k, idesc, (kb | k) != 0);
+          mma_commit_both(&empty[stage]);
           if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
         }
-        mma_commit_pair(map_to_cta(&tfull[acc], 0));
-        mma_commit_pair(map_to_cta(&tfull[acc], 1));
+        mma_commit_both(&tfull[acc]);
+        if (w.column_ends()) mma_commit_both(kempty);
       }
     } else if (lane == 0) {
       // passes the other CTA's drained accumulators on: an arrival on the leader's barrier by the epilogue warps
       // themselves would wait for their stores to reach memory first
       int it = 0;
-      for (int tile = pair; tile < p.num_tiles; tile += npairs, ++it) {
+      for (Int8Walk<KEEP> w(p, pair, npairs); !w.done(p); w.next(p), ++it) {
         if (!mbar_wait(&tempty[it & 1], (it >> 1) & 1)) break;
         mbar_arrive_cluster(map_to_cta(&tempty[it & 1], 0));
       }
     }
   } else {
     // epilogue warps 2..9 -> TMEM lane quadrants 2, 3, 0, 1, 2, 3, 0, 1; warps 2..5 take the even 32-column slices of a
-    // tile, warps 6..9 the odd ones.  A slice of 32 rows passes through a transpose buffer, so that the stores write
-    // whole row segments.
+    // tile, warps 6..9 the odd ones
     const int quad = warp & 3;
     const int chalf = (warp - 2) >> 2;
     constexpr int CH = 32 * sizeof(T_) / 16;   // 16-byte chunks of a row's slice
-    uint4* stg = reinterpret_cast<uint4*>(smem + p.stages * stage_bytes + 256) + (warp - 2) * 32 * CH;
-    // the column scales and biases of the warp's slices, [4][32] each, fetched while the accumulator fills
-    float* sc = reinterpret_cast<float*>(smem + p.stages * stage_bytes + 256 + kI8EpiWarps * 512 * CH) + (warp - 2) * 256;
+    uint4* stg = reinterpret_cast<uint4*>(out) + (warp - 2) * 32 * CH;
+    float* sc = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(bars) + 256) + (warp - 2) * 256;
     const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + chalf * 32;
+    const bool has_bias = p.bias != nullptr;
     int it = 0;
-    for (int tile = pair; tile < p.num_tiles; tile += npairs, ++it) {
-      const int mb = tile / p.num_n_tiles, nb = tile % p.num_n_tiles;
+    for (Int8Walk<KEEP> w(p, pair, npairs); !w.done(p); w.next(p), ++it) {
       const int acc = it & 1;
       const uint32_t acc_par = (it >> 1) & 1;
-      const int row0 = mb * 256 + rank * 128 + quad * 32;
+      const int row0 = w.mb * 256 + rank * 128 + quad * 32;
       const float as = row0 + lane < p.M ? __ldg(p.a_scale + row0 + lane) : 0.f;
-      const int cols = min(p.bn, p.N - nb * p.bn) - chalf * 32;   // of the tile, from this warp's first slice on
-      const int first = nb * p.bn + chalf * 32;
-      // this lane's chunk of the first 32 / CH rows of a slice, and how far the next rows are
-      T_* c_lane = static_cast<T_*>(p.C) + (row0 + lane / CH) * p.ldc + (lane % CH) * (16 / sizeof(T_));
-      const long long step = p.ldc * static_cast<long long>(sizeof(T_)) / 16 * (32 / CH);
+      const int cols = min(p.bn, p.N - w.nb * p.bn) - chalf * 32;   // of the tile, from this warp's first slice on
+      const int first = w.nb * p.bn + chalf * 32;
+      if (!KEEP || w.column_starts()) {   // the column scales and biases of the warp's slices, [4][32] each
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = i * 64 + lane;
-        sc[i * 32 + lane] = c < cols ? __ldg(p.w_scale + first + c) : 0.f;
-        sc[128 + i * 32 + lane] = c < cols && p.bias != nullptr ? __ldg(p.bias + first + c) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const int c = i * 64 + lane;
+          sc[i * 32 + lane] = c < cols ? __ldg(p.w_scale + first + c) : 0.f;
+          if (has_bias) sc[128 + i * 32 + lane] = c < cols ? __ldg(p.bias + first + c) : 0.f;
+        }
+        __syncwarp();
       }
-      __syncwarp();
       if (!mbar_wait(&tfull[acc], acc_par)) break;
       tc_fence_after();
       uint32_t r[32];
@@ -365,13 +462,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         const int col0 = first + i * 64, left = min(32, cols - i * 64);   // the same for the whole warp
         float2 v[16];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {   // (acc a_scale) w_scale + bias
+        for (int q = 0; q < 8; ++q) {   // (acc a_scale) w_scale
           const float4 ws = reinterpret_cast<const float4*>(sc + i * 32)[q];
-          const float4 bq = reinterpret_cast<const float4*>(sc + 128 + i * 32)[q];
           const float2 lo = make_float2(static_cast<int>(r[4 * q]), static_cast<int>(r[4 * q + 1]));
           const float2 hi = make_float2(static_cast<int>(r[4 * q + 2]), static_cast<int>(r[4 * q + 3]));
-          v[2 * q] = fma2(mul_f32x2(lo, both(as)), make_float2(ws.x, ws.y), make_float2(bq.x, bq.y));
-          v[2 * q + 1] = fma2(mul_f32x2(hi, both(as)), make_float2(ws.z, ws.w), make_float2(bq.z, bq.w));
+          v[2 * q] = mul_f32x2(mul_f32x2(lo, both(as)), make_float2(ws.x, ws.y));
+          v[2 * q + 1] = mul_f32x2(mul_f32x2(hi, both(as)), make_float2(ws.z, ws.w));
         }
         const bool more = (i + 1) * 64 < cols;
         if (more) {
@@ -381,7 +477,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&tempty[acc]);
         }
-        // row `lane`, chunk q at q ^ (a function of the row): conflict-free both ways
+        if (has_bias) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 bq = reinterpret_cast<const float4*>(sc + 128 + i * 32)[q];
+            v[2 * q] = add2(v[2 * q], make_float2(bq.x, bq.y));
+            v[2 * q + 1] = add2(v[2 * q + 1], make_float2(bq.z, bq.w));
+          }
+        }
+        if (lane == 0) tma_store_read();   // the slice before has left the staging rows
+        __syncwarp();
 #pragma unroll
         for (int q = 0; q < CH; ++q) {
           uint4 pk;
@@ -393,30 +498,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
                             __float_as_uint(v[q * 2 + 1].y));
           stg[lane * CH + (q ^ int8_swz<CH>(lane))] = pk;
         }
-        __syncwarp();
         if (p.vec && left == 32) {
-          uint4* dst = reinterpret_cast<uint4*>(c_lane + col0);
-#pragma unroll
-          for (int j = 0; j < CH; ++j, dst += step) {
-            const int rr = j * (32 / CH) + lane / CH;
-            if (row0 + rr < p.M) *dst = stg[rr * CH + ((lane % CH) ^ int8_swz<CH>(rr))];
-          }
-        } else {   // rows of C that do not start on 16 bytes, and the last columns: lane = column
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0 && row0 < p.M) tma_store_2d(&maps.c, stg, col0, row0);
+        } else {   // rows of C that do not start on 16 bytes, and the last columns (a store ends at 16 bytes): lane = column
+          __syncwarp();
           constexpr int E = 16 / sizeof(T_);
           const int rows = min(32, p.M - row0);
           for (int rr = 0; rr < rows; ++rr)
             if (lane < left)
               (static_cast<T_*>(p.C) + (row0 + rr) * p.ldc + col0)[lane] =
                   reinterpret_cast<const T_*>(stg + rr * CH + ((lane / E) ^ int8_swz<CH>(rr)))[lane % E];
+          __syncwarp();
         }
         if (more) tmem_wait_ld();
-        __syncwarp();
       }
       if (cols <= 0) {   // a narrow last tile has no slice for these warps
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[acc]);
       }
     }
+    if (lane == 0) tma_store_done();
   }
   tc_fence_before();
   __syncthreads();

@@ -369,6 +369,19 @@ bool make_tmap_s8(CUtensorMap* m, const void* ptr, long long rows, long long col
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Output matrix [rows, cols], box = 32 x 32; 64-byte swizzle for 2-byte elements, 128-byte for 4-byte ones.
+bool make_tmap_out(CUtensorMap* m, void* ptr, long long rows, int cols, long long ld, int es) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+  cuuint32_t box[2] = {32, 32};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, ptr, dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, es == 2 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A warp per row where there are enough rows to fill the SMs, else a block per row.
 template <typename T_>
 void launch_quantize(const T_* x, long long ldx, long long M, int K, void* q, long long ldq, float* scale,
@@ -458,18 +471,33 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   p.C = C;
   p.ldc = ldc;
   p.vec = ldc * (out_dtype == MATE_BF16 ? 2 : 4) % 16 == 0;
-  const uint32_t sb = int8_stage_bytes(p.bn);
-  // the epilogue's transpose buffers, scales and biases
-  const uint32_t stage_out = kI8EpiWarps * (32 * 32 * (out_dtype == MATE_BF16 ? 2 : 4) + 1024);
-  p.stages = std::min<int>(8, static_cast<int>((kSmemLimit - 1024 - 256 - stage_out) / sb));
-  CUtensorMap ta, tb;
-  if (!make_tmap_s8(&ta, A, M, K, lda, 128) || !make_tmap_s8(&tb, Wt, N, K, ldw, p.bn / 2)) return MATE_ERR_CUDA;
-  const size_t smem = 1024 + (size_t)p.stages * sb + 256 + stage_out;
-  auto kernel = out_dtype == MATE_BF16 ? gemm_int8_pair_kernel<__nv_bfloat16> : gemm_int8_pair_kernel<float>;
+  // Keep W in shared memory where that is the shorter way: its tiles take 1 / kI8KeepGain of the others' time, but the
+  // pairs share out whole column tiles.
+  constexpr double kI8KeepGain = 1.2;
+  const int mblocks = ceil_div(M, 256);
+  int pairs = std::min(p.num_tiles, pairs_all);
+  p.slots = std::min(p.num_n_tiles, pairs_all);
+  p.groups = std::min(pairs_all / p.slots, mblocks);
+  const long long kept_tiles = (long long)ceil_div(p.num_n_tiles, p.slots) * ceil_div(mblocks, p.groups);
+  const bool keep = K <= kI8KeepK && p.bn == 256 && kept_tiles < kI8KeepGain * ceil_div(p.num_tiles, pairs);
+  if (keep) pairs = p.slots * p.groups;
+  const int es = out_dtype == MATE_BF16 ? 2 : 4;
+  const uint32_t sb = int8_stage_bytes(p.bn, keep);
+  const uint32_t fixed = 1024 + int8_kept_bytes(p.bn, K, keep) + int8_out_bytes(es) + kI8Behind;
+  p.stages = std::min<int>(8, static_cast<int>((kSmemLimit - fixed) / sb));
+  Int8Maps maps;
+  if (!make_tmap_s8(&maps.a, A, M, K, lda, 128) || !make_tmap_s8(&maps.w, Wt, N, K, ldw, p.bn / 2)) return MATE_ERR_CUDA;
+  if (p.vec) {
+    if (!make_tmap_out(&maps.c, C, M, N, ldc, es)) return MATE_ERR_CUDA;
+  } else {
+    maps.c = maps.a;   // never used
+  }
+  const size_t smem = fixed + (size_t)p.stages * sb;
+  auto kernel = es == 2 ? (keep ? gemm_int8_pair_kernel<__nv_bfloat16, true> : gemm_int8_pair_kernel<__nv_bfloat16, false>)
+                        : (keep ? gemm_int8_pair_kernel<float, true> : gemm_int8_pair_kernel<float, false>);
   if (!set_smem(kernel, smem)) return MATE_ERR_CUDA;
-  const int pairs = std::min(p.num_tiles, pairs_all);
   trace_begin(MATE_K_PROJECT_INT8, st);
-  kernel<<<2 * pairs, kI8Threads, smem, st>>>(ta, tb, p);
+  kernel<<<2 * pairs, kI8Threads, smem, st>>>(maps, p);
   MATE_LAUNCH_CHECK();
   return MATE_OK;
 }

@@ -325,7 +325,8 @@ def test_quantize_rows_ties_and_edges():
 
 
 INT8 = [(1, 16, 1), (1, 1024, 96), (2, 2048, 1001), (5, 100, 37), (8, 4096, 4096), (9, 1040, 513), (16, 512, 264), (17, 256, 256),
-        (64, 333, 2048), (129, 128, 255), (257, 144, 288), (300, 1024, 1000), (513, 2048, 520), (1000, 80, 4368)]
+        (64, 333, 2048), (129, 128, 255), (257, 144, 288), (300, 1024, 1000), (513, 2048, 520), (1000, 80, 4368),
+        (2000, 1024, 300), (600, 48, 19240), (10000, 250, 600), (4000, 1025, 777)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
