@@ -67,6 +67,11 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t u) {
   return __bfloat1622float2(v);
 }
 
+// unpack_bf16x2 by shift and mask (a bf16 is the upper half of its fp32 value).
+__device__ __forceinline__ float2 bf16_pair(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
 // Two fp32 values to an fp16 pair (round to nearest; magnitudes beyond the fp16 range saturate to
 // +-65504 instead of becoming infinite).
 __device__ __forceinline__ uint32_t pack_f16x2_sat(float lo, float hi) {

@@ -12,13 +12,19 @@ namespace mate {
 // Rows to int8: scale = max|x| / 127 (fp32), q = x / scale to the nearest integer, ties to even.
 // ---------------------------------------------------------------------------------------------------
 
-// x / s to the nearest integer k for |x| <= 127.5 s: t = x (1/s) is off by at most 127 * 2^-23 < 2^-15, so rounding t
-// (by adding 1.5 * 2^23, which leaves k in the sum's low byte) is right unless t is within 2^-15 of a midpoint.
-__device__ __forceinline__ float quant_near(float x, float inv, uint32_t* k) {
-  const float t = x * inv;
-  const float m = t + 12582912.f;
-  *k = __float_as_uint(m);
-  return fabsf(t - (m - 12582912.f));   // distance from the integer taken
+// x / s to the nearest integer k for two |x| <= 127.5 s: t = x (1/s) is off by at most 127 * 2^-23 < 2^-15, so rounding t
+// (by adding 1.5 * 2^23, which leaves k in the sum's low byte) is right unless t is within 2^-15 of a midpoint.  off: the
+// largest distance from the integer taken so far.
+__device__ __forceinline__ float2 quant_near(float2 x, float inv, float* off) {
+  const float2 t = mul_f32x2(x, both(inv));
+  const float2 m = add2(t, both(12582912.f));
+  const float2 d = fma2(add2(m, both(-12582912.f)), both(-1.f), t);
+  *off = fmaxf(*off, fmaxf(fabsf(d.x), fabsf(d.y)));
+  return m;
+}
+__device__ __forceinline__ uint32_t quant_bytes(float2 lo, float2 hi) {
+  return __byte_perm(__byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x0040),
+                     __byte_perm(__float_as_uint(hi.x), __float_as_uint(hi.y), 0x0040), 0x5410);
 }
 constexpr float kQuantMid = 0.5f - 1.f / 32768;
 
@@ -37,20 +43,6 @@ constexpr float kQuantTiny = 1e-30f;   // scales below: 1 / s may overflow, the 
 __device__ __forceinline__ int quant_round_tiny(float x, float s) {
   if (s == 0.f) return 0;   // a row of zeros, or of values whose scale rounds to zero
   return static_cast<int>(fmin(fmax(rint(static_cast<double>(x) / static_cast<double>(s)), -127.0), 127.0));
-}
-
-// Four values to four bytes.
-__device__ __forceinline__ uint32_t quant_pack(float a, float b, float c, float d, float s, float inv) {
-  uint32_t x, y, z, w;
-  const float off = fmaxf(fmaxf(quant_near(a, inv, &x), quant_near(b, inv, &y)),
-                          fmaxf(quant_near(c, inv, &z), quant_near(d, inv, &w)));
-  if (off > kQuantMid) {
-    x = quant_round(a, s, inv);
-    y = quant_round(b, s, inv);
-    z = quant_round(c, s, inv);
-    w = quant_round(d, s, inv);
-  }
-  return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
 }
 
 constexpr int kQuantHeld = 8;   // 16-byte vectors of a row that a thread holds between its two passes
@@ -80,11 +72,15 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const T_* __restr
         mx = max(mx, max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu)));
     };
 #pragma unroll
-    for (int j = 0; j < kQuantHeld; ++j)
-      if (t + j * G < nv) h[j] = __ldg(reinterpret_cast<const uint4*>(xr) + t + j * G);
+    for (int j = 0; j < kQuantHeld; ++j) {
+      if (j * G >= nv) break;   // the same for all
+      h[j] = t + j * G < nv ? __ldg(reinterpret_cast<const uint4*>(xr) + t + j * G) : make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
-    for (int j = 0; j < kQuantHeld; ++j)
-      if (t + j * G < nv) take(h[j]);
+    for (int j = 0; j < kQuantHeld; ++j) {
+      if (j * G >= nv) break;
+      take(h[j]);
+    }
     for (int j = t + kQuantHeld * G; j < nv; j += G) take(__ldg(reinterpret_cast<const uint4*>(xr) + j));
     if constexpr (sizeof(T_) == 2) mx = max(mx << 16, mx & 0xffff0000u);
     for (int c = nv * V + t; c < K; c += G) mx = max(mx, __float_as_uint(to_f32(xr[c])) & 0x7fffffffu);
@@ -104,20 +100,33 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const T_* __restr
       continue;
     }
     const float inv = 1.f / s;
-    auto put = [&](int j, const uint4& u) {
+    auto put = [&](int j, const uint4& u) {   // whether a value next to a midpoint is among them
+      float off = 0.f;
       if constexpr (sizeof(T_) == 2) {
-        const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y), c = unpack_bf16x2(u.z), d = unpack_bf16x2(u.w);
-        reinterpret_cast<uint2*>(qr)[j] =
-            make_uint2(quant_pack(a.x, a.y, b.x, b.y, s, inv), quant_pack(c.x, c.y, d.x, d.y, s, inv));
+        const float2 a = quant_near(bf16_pair(u.x), inv, &off), b = quant_near(bf16_pair(u.y), inv, &off);
+        const float2 c = quant_near(bf16_pair(u.z), inv, &off), d = quant_near(bf16_pair(u.w), inv, &off);
+        reinterpret_cast<uint2*>(qr)[j] = make_uint2(quant_bytes(a, b), quant_bytes(c, d));
       } else {
-        reinterpret_cast<uint32_t*>(qr)[j] = quant_pack(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z),
-                                                        __uint_as_float(u.w), s, inv);
+        const float2 a = quant_near(make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), inv, &off);
+        const float2 b = quant_near(make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), inv, &off);
+        reinterpret_cast<uint32_t*>(qr)[j] = quant_bytes(a, b);
       }
+      return off > kQuantMid;
     };
+    // the few vectors with such a value (one value in about 16,000) are done again, one by one
+    auto again = [&](int j) {
+#pragma unroll 1
+      for (int e = 0; e < V; ++e) qr[j * V + e] = static_cast<int8_t>(quant_round(to_f32(xr[j * V + e]), s, inv));
+    };
+    unsigned redo = 0;
 #pragma unroll
-    for (int j = 0; j < kQuantHeld; ++j)
-      if (t + j * G < nv) put(t + j * G, h[j]);
-    for (int j = t + kQuantHeld * G; j < nv; j += G) put(j, __ldg(reinterpret_cast<const uint4*>(xr) + j));
+    for (int j = 0; j < kQuantHeld; ++j) {
+      if (j * G >= nv) break;
+      if (t + j * G < nv && put(t + j * G, h[j])) redo |= 1u << j;
+    }
+    for (int j = t + kQuantHeld * G; j < nv; j += G)
+      if (put(j, __ldg(reinterpret_cast<const uint4*>(xr) + j))) again(j);
+    for (; redo != 0; redo &= redo - 1) again(t + (__ffs(redo) - 1) * G);
     for (int c = nv * V + t; c < K; c += G) qr[c] = static_cast<int8_t>(quant_round(to_f32(xr[c]), s, inv));
   }
 }
