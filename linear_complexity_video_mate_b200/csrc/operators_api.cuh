@@ -63,9 +63,45 @@ mate_status fill_qk(const mate_qk_config* c, const void* x, long long ldx, const
   return MATE_OK;
 }
 
-int qk_blocks(const QkParams& p) {
-  return static_cast<int>(std::min<long long>((p.rows + kQkWarps - 1) / kQkWarps,
-                                              std::min(kQkMaxBlocks, 8 * device_sms())));
+// The kernel for a head's size and pairing: V channels per 16-byte unit, units of 32 lanes (fp32 heads of more than 128
+// channels: two per lane), a power of two of lanes per head.
+template <typename T_, int MODE, bool BWD>
+void (*qk_kernel_of(int units))(QkParams) {
+#define MATE_QK(NV, G) (BWD ? qk_norm_rope_bwd_kernel<T_, MODE, NV, G> : qk_norm_rope_kernel<T_, MODE, NV, G>)
+  if constexpr (sizeof(T_) == 4)
+    if (units > 32) return MATE_QK(2, 32);
+  if (units > 16) return MATE_QK(1, 32);
+  if (units > 8) return MATE_QK(1, 16);
+  if (units > 4) return MATE_QK(1, 8);
+  return MATE_QK(1, 4);
+#undef MATE_QK
+}
+
+template <bool BWD>
+mate_status launch_qk(int kid, const mate_qk_config* c, QkParams p, cudaStream_t st, int* blocks) {
+  const int es = c->dtype == MATE_BF16 ? 2 : 4, V = 16 / es, units = c->tp / V;
+  // halves whose axes are whole 8-byte units pair up inside a lane
+  const int mode = c->pairing == 0 ? kQkAdjacent : (c->rt % V || c->rh % V || c->rw % V) ? kQkAny : kQkHalves;
+  void (*kernel)(QkParams);
+  if (es == 2)
+    kernel = mode == kQkAdjacent ? qk_kernel_of<__nv_bfloat16, kQkAdjacent, BWD>(units)
+                                 : mode == kQkHalves ? qk_kernel_of<__nv_bfloat16, kQkHalves, BWD>(units)
+                                                     : qk_kernel_of<__nv_bfloat16, kQkAny, BWD>(units);
+  else
+    kernel = mode == kQkAdjacent ? qk_kernel_of<float, kQkAdjacent, BWD>(units)
+                                 : mode == kQkHalves ? qk_kernel_of<float, kQkHalves, BWD>(units)
+                                                     : qk_kernel_of<float, kQkAny, BWD>(units);
+  // few rows: several warps share a row's heads
+  const long long warps = 16LL * device_sms();
+  const int per = 32 / std::min(32, units > 16 ? 32 : units > 8 ? 16 : units > 4 ? 8 : 4);
+  const int iters = std::max(ceil_div(c->hq, per), ceil_div(c->hk, per));
+  p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>(iters, warps / p.rows)));
+  *blocks = static_cast<int>(std::min<long long>((p.rows * p.splits + kQkWarps - 1) / kQkWarps,
+                                                 std::min(kQkMaxBlocks, 8 * device_sms())));
+  trace_begin(kid, st);
+  kernel<<<*blocks, kQkWarps * 32, 0, st>>>(p);
+  MATE_LAUNCH_CHECK();
+  return MATE_OK;
 }
 
 }  // namespace
@@ -100,11 +136,8 @@ mate_status mate_qk_norm_rope(const void* qkv, long long ldi, const float* wq, c
   p.copy_v = cfg->hv > 0 && out != qkv;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   t_launches = 0;
-  trace_begin(MATE_K_QK_NORM_ROPE, st);
-  if (cfg->dtype == MATE_BF16) qk_norm_rope_kernel<__nv_bfloat16><<<qk_blocks(p), kQkWarps * 32, 0, st>>>(p);
-  else qk_norm_rope_kernel<float><<<qk_blocks(p), kQkWarps * 32, 0, st>>>(p);
-  MATE_LAUNCH_CHECK();
-  return MATE_OK;
+  int blocks = 0;
+  return launch_qk<false>(MATE_K_QK_NORM_ROPE, cfg, p, st, &blocks);
 }
 
 size_t mate_qk_norm_rope_backward_workspace_bytes(const mate_qk_config* cfg) {
@@ -134,11 +167,8 @@ mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, const flo
   p.copy_v = cfg->hv > 0 && dqkv != dout;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   t_launches = 0;
-  const int blocks = qk_blocks(p);
-  trace_begin(MATE_K_QK_NORM_ROPE_BWD, st);
-  if (cfg->dtype == MATE_BF16) qk_norm_rope_bwd_kernel<__nv_bfloat16><<<blocks, kQkWarps * 32, 0, st>>>(p);
-  else qk_norm_rope_bwd_kernel<float><<<blocks, kQkWarps * 32, 0, st>>>(p);
-  MATE_LAUNCH_CHECK();
+  int blocks = 0;
+  MATE_TRY(launch_qk<true>(MATE_K_QK_NORM_ROPE_BWD, cfg, p, st, &blocks));
   if (dwq != nullptr || dwk != nullptr) {
     trace_begin(MATE_K_QK_WEIGHT_GRAD, st);
     qk_weight_grad_kernel<<<ceil_div(2 * cfg->tp, 8), 256, 0, st>>>(p.part, blocks, cfg->tp, dwq, dwk);

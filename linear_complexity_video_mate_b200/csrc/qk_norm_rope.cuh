@@ -5,6 +5,12 @@
 // each channel pair (u, v) by the angle of the token's position along one grid axis:
 //   (u, v) -> (u cos - v sin, v cos + u sin).
 // Backward: dy = R^T dz,  dw = sum of dy x r over rows and heads,  g = dy w,  dx = r (g - x r mean(g x r)).
+//
+// Bound by HBM: every value is read and written once.  A warp takes one row at a time.  G lanes (a power of two) share
+// a head vector, each with PAIRS channel pairs of it, and 32 / G heads are worked on at a time; a lane has the same
+// channels in every head, so the token's cos and sin and the weights of those channels are fetched once per row and
+// once per warp.  Both halves of every pair are in one lane: adjacent channels as 16-byte vectors, halves as two
+// vectors of half that width, so the rotation needs no exchange; the norm is a sum over G lanes.
 #pragma once
 #include "common.cuh"
 #include "mamba_extras.cuh"   // to_f32, from_f32
@@ -28,44 +34,12 @@ struct QkParams {
   int pairing;         // 0: channels 2i, 2i+1 of an axis block; 1: channels i, i + r/2
   float eps;
   int copy_v;
+  int splits;          // warps that share a row's heads
 };
 
 constexpr int kQkMaxDim = 256;
 constexpr int kQkWarps = 8;
 constexpr int kQkMaxBlocks = 1184;   // 8 blocks per SM: also the number of partial weight gradients
-
-// The partner of channel c and the (cos, signed sin) of its rotation: z_c = y_c cos + s y_partner sin with
-// s = -1 for the pair's first channel, +1 for its second.  Channels behind the rotated ones: (c, 1, 0).
-__device__ __forceinline__ void qk_pair(const QkParams& p, int c, int t, int h, int w, int* partner, float* co,
-                                        float* si) {
-  const float2* tab;
-  int r;
-  int c0 = 0;
-  if (c < p.rt) {
-    r = p.rt;
-    tab = p.tab_t + (long long)t * (r / 2);
-  } else if (c < p.rt + p.rh) {
-    c0 = p.rt;
-    r = p.rh;
-    tab = p.tab_h + (long long)h * (r / 2);
-  } else if (c < p.rt + p.rh + p.rw) {
-    c0 = p.rt + p.rh;
-    r = p.rw;
-    tab = p.tab_w + (long long)w * (r / 2);
-  } else {
-    *partner = c;
-    *co = 1.f;
-    *si = 0.f;
-    return;
-  }
-  const int i = c - c0;
-  const int pi = p.pairing == 0 ? i >> 1 : (i < r / 2 ? i : i - r / 2);
-  const bool second = p.pairing == 0 ? (i & 1) : i >= r / 2;
-  const float2 cs = __ldg(tab + pi);
-  *partner = c0 + (p.pairing == 0 ? (i ^ 1) : (second ? i - r / 2 : i + r / 2));
-  *co = cs.x;
-  *si = second ? cs.y : -cs.y;
-}
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -73,95 +47,368 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// One warp per row; lanes walk the channels of one head after another.
-template <typename T_>
-__global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_kernel(QkParams p) {
-  __shared__ float s_y[kQkWarps][kQkMaxDim];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = p.T * p.H * p.W;
-  for (long long row = (long long)blockIdx.x * kQkWarps + warp; row < p.rows; row += (long long)gridDim.x * kQkWarps) {
-    const int tok = static_cast<int>(row % n);
-    const int w = tok % p.W, h = (tok / p.W) % p.H, t = tok / (p.W * p.H);
-    const T_* x = static_cast<const T_*>(p.x) + row * p.ldx;
-    T_* out = static_cast<T_*>(p.out) + row * p.ldo;
-    for (int head = 0; head < p.hq + p.hk; ++head) {
-      const float* wt = head < p.hq ? p.wq : p.wk;
-      float ss = 0.f;
-      for (int c = lane; c < p.tp; c += 32) {
-        const float v = to_f32(x[head * p.tp + c]);
-        s_y[warp][c] = v;
-        ss = fmaf(v, v, ss);
-      }
-      const float r = rsqrtf(warp_sum(ss) / p.tp + p.eps);
-      for (int c = lane; c < p.tp; c += 32) s_y[warp][c] *= wt != nullptr ? r * wt[c] : r;
-      __syncwarp();
-      for (int c = lane; c < p.tp; c += 32) {
-        int pc;
-        float co, si;
-        qk_pair(p, c, t, h, w, &pc, &co, &si);
-        out[head * p.tp + c] = from_f32<T_>(s_y[warp][c] * co + s_y[warp][pc] * si);
-      }
-      __syncwarp();
+// How a lane's 16-byte units lie in a head and how their channels pair up.
+enum : int {
+  kQkAdjacent = 0,   // 16 contiguous bytes; channels 2i, 2i + 1 pair up
+  kQkHalves = 1,     // 8 bytes of the first half of an axis' channels and the 8 bytes they pair with (r a multiple of 16 bytes)
+  kQkAny = 2         // 16 contiguous bytes, partners through shared memory (halves that 8-byte units do not divide)
+};
+
+// Values of one lane: NV units of V channels, as P pairs of fp32 values each.
+template <typename T_, int MODE, int NV>
+struct QkLane {
+  static constexpr int V = 16 / sizeof(T_), P = V / 2, HV = V / 2;
+  static constexpr int C = MODE == kQkAny ? V : P;   // (cos, sin) entries per unit
+  float2 w[2][NV][P];      // weights of q and k heads
+  float2 cs[NV][C];        // the row's cos and sin (kQkHalves: first all cos, then all sin of the unit's pairs)
+  int c[NV][2];            // first channel of the unit (kQkHalves: of its two halves)
+  int axis[NV][C], idx[NV][C], partner[MODE == kQkAny ? NV : 1][MODE == kQkAny ? V : 1];
+  bool on[NV];
+
+  // Axis and table entry of channel c (axis 3: not rotated), and the channel it pairs with.
+  static __device__ __forceinline__ int locate(const QkParams& p, int ch, int* i, int* other, bool* second) {
+    const int b1 = p.rt, b2 = b1 + p.rh, b3 = b2 + p.rw;
+    const int ax = ch < b1 ? 0 : ch < b2 ? 1 : ch < b3 ? 2 : 3;
+    const int c0 = ax == 0 ? 0 : ax == 1 ? b1 : ax == 2 ? b2 : b3;
+    const int half = (ax == 0 ? p.rt : ax == 1 ? p.rh : ax == 2 ? p.rw : p.tp - b3) / 2, k = ch - c0;
+    if (p.pairing == 0) {
+      *i = k >> 1;
+      *second = k & 1;
+      *other = ch ^ 1;
+    } else {
+      *second = k >= half;
+      *i = *second ? k - half : k;
+      *other = *second ? ch - half : ch + half;
     }
-    if (p.copy_v)
-      for (int c = (p.hq + p.hk) * p.tp + lane; c < (p.hq + p.hk + p.hv) * p.tp; c += 32) out[c] = x[c];
+    if (ax == 3) *other = ch;
+    return ax;
+  }
+
+  __device__ __forceinline__ void init(const QkParams& p, int e, int G) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int u = e + n * G;
+      on[n] = u < p.tp / V;
+      int i, o;
+      bool s;
+      if constexpr (MODE == kQkHalves) {
+        // units run over the first halves of the axes' channels, then of the ones that stay
+        int left = on[n] ? u * HV : 0, c0 = 0, r = p.rt;
+        if (left >= r / 2) { left -= r / 2; c0 += r; r = p.rh; }
+        if (c0 == p.rt && r == p.rh && left >= r / 2) { left -= r / 2; c0 += r; r = p.rw; }
+        if (c0 == p.rt + p.rh && r == p.rw && left >= r / 2) { left -= r / 2; c0 += r; r = p.tp - c0; }
+        c[n][0] = c0 + left;
+        c[n][1] = c[n][0] + r / 2;
+      } else {
+        c[n][0] = on[n] ? u * V : 0;
+        c[n][1] = c[n][0] + HV;
+      }
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int ch = c[n][0] + (MODE == kQkAdjacent ? 2 * k : k);
+        axis[n][k] = locate(p, ch, &i, &o, &s);
+        idx[n][k] = i;
+        if constexpr (MODE == kQkAny) partner[n][k] = s ? ~o : o;   // the second of a pair, negated
+      }
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        const int ch = c[n][2 * k / HV] + 2 * k % HV;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float* wt = q == 0 ? p.wq : p.wk;
+          w[q][n][k] = wt != nullptr ? make_float2(__ldg(wt + ch), __ldg(wt + ch + 1)) : both(1.f);
+        }
+      }
+    }
+  }
+
+  // The row's cos and sin of this lane's channels.
+  __device__ __forceinline__ void row(const QkParams& p, int tok) {
+    const int wi = tok % p.W, rest = tok / p.W, hi = rest % p.H, ti = rest / p.H;
+    const float2* t0 = p.tab_t + (long long)ti * (p.rt / 2);
+    const float2* t1 = p.tab_h + (long long)hi * (p.rh / 2);
+    const float2* t2 = p.tab_w + (long long)wi * (p.rw / 2);
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      float2 v[C];
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        const int ax = axis[n][k];
+        v[k] = ax == 3 ? make_float2(1.f, 0.f) : __ldg((ax == 0 ? t0 : ax == 1 ? t1 : t2) + idx[n][k]);
+        if constexpr (MODE == kQkAny)
+          if (partner[n][k] >= 0) v[k].y = -v[k].y;
+      }
+#pragma unroll
+      for (int k = 0; k < C; ++k) {
+        if constexpr (MODE == kQkHalves)
+          cs[n][k] = k < P / 2 ? make_float2(v[2 * k].x, v[2 * k + 1].x)
+                               : make_float2(v[2 * (k - P / 2)].y, v[2 * (k - P / 2) + 1].y);
+        else
+          cs[n][k] = v[k];
+      }
+    }
+  }
+
+  __device__ __forceinline__ uint4 load(const T_* head, int n) const {
+    if constexpr (MODE == kQkHalves) {
+      const uint2 a = __ldg(reinterpret_cast<const uint2*>(head + c[n][0]));
+      const uint2 b = __ldg(reinterpret_cast<const uint2*>(head + c[n][1]));
+      return make_uint4(a.x, a.y, b.x, b.y);
+    } else {
+      return __ldg(reinterpret_cast<const uint4*>(head + c[n][0]));
+    }
+  }
+  __device__ __forceinline__ void store(T_* head, int n, const float2 (&v)[P]) const {
+    uint4 u;
+    if constexpr (sizeof(T_) == 2)
+      u = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y), pack_bf16x2(v[2].x, v[2].y),
+                     pack_bf16x2(v[3].x, v[3].y));
+    else
+      u = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+    if constexpr (MODE == kQkHalves) {
+      *reinterpret_cast<uint2*>(head + c[n][0]) = make_uint2(u.x, u.y);
+      *reinterpret_cast<uint2*>(head + c[n][1]) = make_uint2(u.z, u.w);
+    } else {
+      *reinterpret_cast<uint4*>(head + c[n][0]) = u;
+    }
+  }
+  static __device__ __forceinline__ void unpack(const uint4& u, float2 (&v)[P]) {
+    if constexpr (sizeof(T_) == 2) {
+      v[0] = bf16_pair(u.x);
+      v[1] = bf16_pair(u.y);
+      v[2] = bf16_pair(u.z);
+      v[3] = bf16_pair(u.w);
+    } else {
+      v[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+      v[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+    }
+  }
+
+  // The rotation (BACK: its transpose) of a head, values of all its lanes at once (buf: the head's tp values of scratch).
+  template <bool BACK>
+  __device__ __forceinline__ void rotate(float2 (&v)[NV][P], float* buf) const {
+    if constexpr (MODE == kQkAdjacent) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const float co = cs[n][k].x, si = BACK ? -cs[n][k].y : cs[n][k].y;
+          const float2 a = v[n][k];
+          v[n][k] = make_float2(fmaf(a.x, co, -a.y * si), fmaf(a.y, co, a.x * si));
+        }
+    } else if constexpr (MODE == kQkHalves) {
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int k = 0; k < P / 2; ++k) {
+          const float2 co = cs[n][k], si = cs[n][k + P / 2], ns = make_float2(-si.x, -si.y);
+          const float2 a = v[n][k], b = v[n][k + P / 2];
+          v[n][k] = fma2(a, co, mul_f32x2(b, BACK ? si : ns));
+          v[n][k + P / 2] = fma2(b, co, mul_f32x2(a, BACK ? ns : si));
+        }
+    } else {
+      __syncwarp();   // the head before is read
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+        if (on[n])
+#pragma unroll
+          for (int k = 0; k < P; ++k) *reinterpret_cast<float2*>(buf + c[n][0] + 2 * k) = v[n][k];
+      __syncwarp();
+#pragma unroll
+      for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const int a = partner[n][2 * k], b = partner[n][2 * k + 1];
+          const float pa = buf[a < 0 ? ~a : a], pb = buf[b < 0 ? ~b : b];
+          const float2 ca = cs[n][2 * k], cb = cs[n][2 * k + 1];
+          v[n][k] = make_float2(fmaf(v[n][k].x, ca.x, pa * (BACK ? -ca.y : ca.y)),
+                                fmaf(v[n][k].y, cb.x, pb * (BACK ? -cb.y : cb.y)));
+        }
+    }
+  }
+};
+
+// Sum over the G lanes of a head.
+__device__ __forceinline__ float group_sum(float v, int G) {
+  for (int o = G >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Which of a row's heads a warp works on: unit -> row, part.
+struct QkUnit {
+  int row, part;
+  __device__ __forceinline__ QkUnit(const QkParams& p, long long u) {
+    row = static_cast<int>(u / p.splits);
+    part = static_cast<int>(u - (long long)row * p.splits);
+  }
+};
+
+// Copies the value heads of a row.
+template <typename T_>
+__device__ __forceinline__ void qk_copy_v(const QkParams& p, const T_* src, T_* dst, int part) {
+  constexpr int V = 16 / sizeof(T_);
+  const int c0 = (p.hq + p.hk) * p.tp, nv = p.hv * p.tp / V, step = 32 * p.splits;
+  const uint4* s = reinterpret_cast<const uint4*>(src + c0);
+  uint4* d = reinterpret_cast<uint4*>(dst + c0);
+  for (int v = part * 32 + (threadIdx.x & 31); v < nv; v += 4 * step) {
+    uint4 u[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (v + j * step < nv) u[j] = __ldg(s + v + j * step);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (v + j * step < nv) d[v + j * step] = u[j];
   }
 }
 
-template <typename T_>
-__global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_bwd_kernel(QkParams p) {
-  __shared__ float s_z[kQkWarps][kQkMaxDim];
-  __shared__ float s_x[kQkWarps][kQkMaxDim];
-  __shared__ float s_dw[kQkWarps][2][kQkMaxDim];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = p.T * p.H * p.W;
-  for (int c = lane; c < 2 * kQkMaxDim; c += 32) (&s_dw[warp][0][0])[c] = 0.f;
-  for (long long row = (long long)blockIdx.x * kQkWarps + warp; row < p.rows; row += (long long)gridDim.x * kQkWarps) {
-    const int tok = static_cast<int>(row % n);
-    const int w = tok % p.W, h = (tok / p.W) % p.H, t = tok / (p.W * p.H);
-    const T_* x = static_cast<const T_*>(p.x) + row * p.ldx;
-    const T_* dz = static_cast<const T_*>(p.dz) + row * p.ldz;
-    T_* out = static_cast<T_*>(p.out) + row * p.ldo;
-    for (int head = 0; head < p.hq + p.hk; ++head) {
-      const int kind = head < p.hq ? 0 : 1;
-      const float* wt = kind == 0 ? p.wq : p.wk;
-      float ss = 0.f;
-      for (int c = lane; c < p.tp; c += 32) {
-        const float v = to_f32(x[head * p.tp + c]);
-        s_x[warp][c] = v;
-        s_z[warp][c] = to_f32(dz[head * p.tp + c]);
-        ss = fmaf(v, v, ss);
-      }
-      const float r = rsqrtf(warp_sum(ss) / p.tp + p.eps);
-      __syncwarp();
-      float gx = 0.f;
-      float g[kQkMaxDim / 32];
+template <typename T_, int MODE, int NV, int G>
+__global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_kernel(const QkParams p) {
+  using L = QkLane<T_, MODE, NV>;
+  constexpr int HPW = 32 / G, UN = NV == 1 ? 4 : 2;   // heads at a time, and how many of those are loaded ahead
+  __shared__ float s_buf[MODE == kQkAny ? kQkWarps * 32 * NV * L::V : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G;
+  float* buf = s_buf + (MODE == kQkAny ? (warp * HPW + slot) * (G * NV * L::V) : 0);
+  const int n_tok = p.T * p.H * p.W;
+  const float inv_tp = 1.f / p.tp;
+  L l;
+  l.init(p, lane % G, G);
+  for (long long u = (long long)blockIdx.x * kQkWarps + warp; u < p.rows * p.splits; u += (long long)gridDim.x * kQkWarps) {
+    const QkUnit un(p, u);
+    l.row(p, un.row % n_tok);
+    const T_* x = static_cast<const T_*>(p.x) + un.row * p.ldx;
+    T_* out = static_cast<T_*>(p.out) + un.row * p.ldo;
 #pragma unroll
-      for (int j = 0; j < kQkMaxDim / 32; ++j) {
-        const int c = lane + 32 * j;
-        g[j] = 0.f;
-        if (c < p.tp) {
-          int pc;
-          float co, si;
-          qk_pair(p, c, t, h, w, &pc, &co, &si);
-          const float dy = s_z[warp][c] * co - s_z[warp][pc] * si;   // the transposed rotation
-          const float nx = s_x[warp][c] * r;
-          s_dw[warp][kind][c] += dy * nx;
-          g[j] = wt != nullptr ? dy * wt[c] : dy;
-          gx = fmaf(g[j], nx, gx);
+    for (int kind = 0; kind < 2; ++kind) {
+      const int h0 = kind == 0 ? 0 : p.hq, h1 = kind == 0 ? p.hq : p.hq + p.hk;
+      for (int b = h0 + un.part * HPW + slot; b - slot < h1; b += UN * p.splits * HPW) {
+        uint4 raw[UN][NV];
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+          const int head = b + j * p.splits * HPW;
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+            raw[j][n] = head < h1 && l.on[n] ? l.load(x + head * p.tp, n) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+          const int head = b + j * p.splits * HPW;
+          if (head - slot >= h1) break;   // the same for the warp
+          float2 v[NV][L::P], ss = both(0.f);
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            L::unpack(raw[j][n], v[n]);
+#pragma unroll
+            for (int k = 0; k < L::P; ++k) ss = fma2(v[n][k], v[n][k], ss);
+          }
+          const float r = rsqrtf(fmaf(group_sum(ss.x + ss.y, G), inv_tp, p.eps));
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int k = 0; k < L::P; ++k) v[n][k] = mul_f32x2(mul_f32x2(v[n][k], both(r)), l.w[kind][n][k]);
+          l.template rotate<false>(v, buf);
+          if (head < h1)
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+              if (l.on[n]) l.store(out + head * p.tp, n, v[n]);
         }
       }
-      const float m = warp_sum(gx) / p.tp;
-#pragma unroll
-      for (int j = 0; j < kQkMaxDim / 32; ++j) {
-        const int c = lane + 32 * j;
-        if (c < p.tp) out[head * p.tp + c] = from_f32<T_>(r * (g[j] - s_x[warp][c] * r * m));
-      }
-      __syncwarp();
     }
-    if (p.copy_v)
-      for (int c = (p.hq + p.hk) * p.tp + lane; c < (p.hq + p.hk + p.hv) * p.tp; c += 32) out[c] = dz[c];
+    if (p.copy_v) qk_copy_v(p, x, out, un.part);
   }
+}
+
+template <typename T_, int MODE, int NV, int G>
+__global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_bwd_kernel(const QkParams p) {
+  using L = QkLane<T_, MODE, NV>;
+  constexpr int HPW = 32 / G, UN = NV == 1 ? 2 : 1;
+  __shared__ float s_buf[MODE == kQkAny ? kQkWarps * 32 * NV * L::V : 1];
+  __shared__ float s_dw[kQkWarps][2][kQkMaxDim];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G;
+  float* buf = s_buf + (MODE == kQkAny ? (warp * HPW + slot) * (G * NV * L::V) : 0);
+  const int n_tok = p.T * p.H * p.W;
+  const float inv_tp = 1.f / p.tp;
+  L l;
+  l.init(p, lane % G, G);
+  float2 dw[2][NV][L::P];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+      for (int k = 0; k < L::P; ++k) dw[q][n][k] = both(0.f);
+  for (long long u = (long long)blockIdx.x * kQkWarps + warp; u < p.rows * p.splits; u += (long long)gridDim.x * kQkWarps) {
+    const QkUnit un(p, u);
+    l.row(p, un.row % n_tok);
+    const T_* x = static_cast<const T_*>(p.x) + un.row * p.ldx;
+    const T_* dz = static_cast<const T_*>(p.dz) + un.row * p.ldz;
+    T_* out = static_cast<T_*>(p.out) + un.row * p.ldo;
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      const int h0 = kind == 0 ? 0 : p.hq, h1 = kind == 0 ? p.hq : p.hq + p.hk;
+      for (int b = h0 + un.part * HPW + slot; b - slot < h1; b += UN * p.splits * HPW) {
+        uint4 raw[UN][NV], rawz[UN][NV];
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+          const int head = b + j * p.splits * HPW;
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            const bool ok = head < h1 && l.on[n];
+            raw[j][n] = ok ? l.load(x + head * p.tp, n) : make_uint4(0, 0, 0, 0);
+            rawz[j][n] = ok ? l.load(dz + head * p.tp, n) : make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < UN; ++j) {
+          const int head = b + j * p.splits * HPW;
+          if (head - slot >= h1) break;
+          float2 v[NV][L::P], g[NV][L::P], ss = both(0.f), gx = both(0.f);
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            L::unpack(raw[j][n], v[n]);
+            L::unpack(rawz[j][n], g[n]);
+#pragma unroll
+            for (int k = 0; k < L::P; ++k) ss = fma2(v[n][k], v[n][k], ss);
+          }
+          const float r = rsqrtf(fmaf(group_sum(ss.x + ss.y, G), inv_tp, p.eps));
+          l.template rotate<true>(g, buf);
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int k = 0; k < L::P; ++k) {
+              v[n][k] = mul_f32x2(v[n][k], both(r));
+              dw[kind][n][k] = fma2(g[n][k], v[n][k], dw[kind][n][k]);
+              g[n][k] = mul_f32x2(g[n][k], l.w[kind][n][k]);
+              gx = fma2(g[n][k], v[n][k], gx);
+            }
+          const float m = -group_sum(gx.x + gx.y, G) * inv_tp;
+#pragma unroll
+          for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int k = 0; k < L::P; ++k) g[n][k] = mul_f32x2(fma2(v[n][k], both(m), g[n][k]), both(r));
+          if (head < h1)
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+              if (l.on[n]) l.store(out + head * p.tp, n, g[n]);
+        }
+      }
+    }
+    if (p.copy_v) qk_copy_v(p, dz, out, un.part);
+  }
+  // the block's weight gradients: the warp's head slots, then the warps, in order
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+      for (int k = 0; k < L::P; ++k) {
+        float2 d = dw[q][n][k];
+        for (int o = G; o < 32; o <<= 1) {
+          d.x += __shfl_xor_sync(0xffffffffu, d.x, o);
+          d.y += __shfl_xor_sync(0xffffffffu, d.y, o);
+        }
+        if (slot == 0 && l.on[n])
+          *reinterpret_cast<float2*>(&s_dw[warp][q][l.c[n][2 * k / L::HV] + 2 * k % L::HV]) = d;
+      }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * p.tp; i += blockDim.x) {
     const int kind = i / p.tp, c = i % p.tp;
