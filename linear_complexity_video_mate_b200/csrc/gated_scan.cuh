@@ -569,26 +569,4 @@ __global__ void __launch_bounds__(kGsThreads, 2)
   }
 }
 
-// dbias [D] = the tiles' partial sums, added in their order (the same result on every run): a block takes 32 channels,
-// each of its 32 warps every 32nd part.
-__global__ void __launch_bounds__(1024) gated_scan_bias_kernel(const float* __restrict__ part, int parts, int D,
-                                                               float* __restrict__ dbias) {
-  __shared__ float s[32][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  float v = 0.f;
-  if (c < D) {
-#pragma unroll 8
-    for (int k = warp; k < parts; k += 32) v += part[(long long)k * D + c];
-  }
-  s[warp][lane] = v;
-  __syncthreads();
-  if (warp == 0 && c < D) {
-    v = 0.f;
-#pragma unroll
-    for (int k = 0; k < 32; ++k) v += s[k][lane];
-    dbias[c] = v;
-  }
-}
-
 }  // namespace mate

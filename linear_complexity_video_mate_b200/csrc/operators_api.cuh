@@ -96,8 +96,9 @@ mate_status launch_qk(int kid, const mate_qk_config* c, QkParams p, cudaStream_t
   const int per = 32 / std::min(32, units > 16 ? 32 : units > 8 ? 16 : units > 4 ? 8 : 4);
   const int iters = std::max(ceil_div(c->hq, per), ceil_div(c->hk, per));
   p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>(iters, warps / p.rows)));
+  // the backward pass with as many blocks as are resident, so that their weight gradients are few
   *blocks = static_cast<int>(std::min<long long>((p.rows * p.splits + kQkWarps - 1) / kQkWarps,
-                                                 std::min(kQkMaxBlocks, 8 * device_sms())));
+                                                 BWD ? std::min(kQkMaxParts, 2 * device_sms()) : 8 * device_sms()));
   trace_begin(kid, st);
   kernel<<<*blocks, kQkWarps * 32, 0, st>>>(p);
   MATE_LAUNCH_CHECK();
@@ -142,7 +143,7 @@ mate_status mate_qk_norm_rope(const void* qkv, long long ldi, const float* wq, c
 
 size_t mate_qk_norm_rope_backward_workspace_bytes(const mate_qk_config* cfg) {
   if (check_qk(cfg) != MATE_OK) return 0;
-  return (size_t)kQkMaxBlocks * 2 * cfg->tp * sizeof(float);
+  return (size_t)kQkMaxParts * 2 * cfg->tp * sizeof(float);
 }
 
 mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, const float* wq, const float* wk,
@@ -171,7 +172,7 @@ mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, const flo
   MATE_TRY(launch_qk<true>(MATE_K_QK_NORM_ROPE_BWD, cfg, p, st, &blocks));
   if (dwq != nullptr || dwk != nullptr) {
     trace_begin(MATE_K_QK_WEIGHT_GRAD, st);
-    qk_weight_grad_kernel<<<ceil_div(2 * cfg->tp, 8), 256, 0, st>>>(p.part, blocks, cfg->tp, dwq, dwk);
+    sum_parts_kernel<<<ceil_div(2 * cfg->tp, 32), 1024, 0, st>>>(p.part, blocks, 2 * cfg->tp, dwq, cfg->tp, dwk);
     MATE_LAUNCH_CHECK();
   }
   return MATE_OK;
@@ -374,7 +375,7 @@ mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g
                         bf ? sizeof(GsSmem<__nv_bfloat16, 3>) : sizeof(GsSmem<float, 3>), p, bf, s, ws, st));
   if (dbias != nullptr) {
     trace_begin(MATE_K_GATED_SCAN_BIAS, st);
-    gated_scan_bias_kernel<<<ceil_div(cfg->D, 32), 1024, 0, st>>>(s.dbias_part, cfg->B * p.tiles, cfg->D, dbias);
+    sum_parts_kernel<<<ceil_div(cfg->D, 32), 1024, 0, st>>>(s.dbias_part, cfg->B * p.tiles, cfg->D, dbias, cfg->D, nullptr);
     MATE_LAUNCH_CHECK();
   }
   return MATE_OK;

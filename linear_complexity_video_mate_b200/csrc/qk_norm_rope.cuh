@@ -39,12 +39,32 @@ struct QkParams {
 
 constexpr int kQkMaxDim = 256;
 constexpr int kQkWarps = 8;
-constexpr int kQkMaxBlocks = 1184;   // 8 blocks per SM: also the number of partial weight gradients
+constexpr int kQkMaxParts = 512;     // blocks of the backward pass, with a partial sum of the weight gradients each
 
-__device__ __forceinline__ float warp_sum(float v) {
+// out [cols] = the parts' rows of [parts][cols], added in a fixed order (the same result on every run): a block takes 32
+// columns, each of its 32 warps every 32nd part.  Columns from `split` on go to out2; either may be null.
+__global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict__ part, int parts, int cols,
+                                                         float* __restrict__ out, int split, float* __restrict__ out2) {
+  __shared__ float s[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < cols) {
+#pragma unroll 8
+    for (int k = warp; k < parts; k += 32) v += part[(long long)k * cols + c];
+  }
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+    v = 0.f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+    for (int k = 0; k < 32; ++k) v += s[k][lane];
+    if (c < split) {
+      if (out != nullptr) out[c] = v;
+    } else if (out2 != nullptr) {
+      out2[c - split] = v;
+    }
+  }
 }
 
 // How a lane's 16-byte units lie in a head and how their channels pair up.
@@ -262,9 +282,9 @@ __device__ __forceinline__ void qk_copy_v(const QkParams& p, const T_* src, T_* 
 }
 
 template <typename T_, int MODE, int NV, int G>
-__global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kQkWarps * 32, 2) qk_norm_rope_kernel(const QkParams p) {
   using L = QkLane<T_, MODE, NV>;
-  constexpr int HPW = 32 / G, UN = NV == 1 ? 4 : 2;   // heads at a time, and how many of those are loaded ahead
+  constexpr int HPW = 32 / G, UN = NV == 1 ? 8 : 2;   // heads at a time, and how many of those are loaded ahead
   __shared__ float s_buf[MODE == kQkAny ? kQkWarps * 32 * NV * L::V : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G;
   float* buf = s_buf + (MODE == kQkAny ? (warp * HPW + slot) * (G * NV * L::V) : 0);
@@ -416,19 +436,6 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_bwd_kernel(const Q
     for (int k = 0; k < kQkWarps; ++k) v += s_dw[k][kind][c];
     p.part[(long long)blockIdx.x * 2 * p.tp + i] = v;
   }
-}
-
-// dwq | dwk [tp] = the blocks' partial sums, added in block order (the same result on every run).
-__global__ void __launch_bounds__(256) qk_weight_grad_kernel(const float* __restrict__ part, int blocks, int tp,
-                                                             float* __restrict__ dwq, float* __restrict__ dwk) {
-  const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (i >= 2 * tp) return;
-  float v = 0.f;
-  for (int b = lane; b < blocks; b += 32) v += part[(long long)b * 2 * tp + i];
-  v = warp_sum(v);
-  float* d = i < tp ? dwq : dwk;
-  if (lane == 0 && d != nullptr) d[i < tp ? i : i - tp] = v;
 }
 
 // (cos, sin) of (start + p) theta^(-2 i / dims), p < count, i < dims / 2, the angle in 64 bits.
