@@ -54,6 +54,22 @@ __host__ __device__ __forceinline__ int raster_to_scan(int r, int T, int H, int 
   }
 }
 
+// Division of 0 <= n < 2^31 by a fixed d >= 1 as a product: with l = ceil(log2 d), m = floor(2^(31+l) / d) + 1 is below
+// 2^32 and n m / 2^(31+l) exceeds n / d by less than 1 / d, so its integer part is the quotient.
+struct FastDiv {
+  unsigned d = 1, m = 0, shift = 0;   // d = 1: the quotient is n
+  FastDiv() = default;
+  explicit FastDiv(unsigned div) : d(div) {
+    unsigned l = 0;
+    while ((1ull << l) < div) ++l;
+    if (l > 0) {
+      m = static_cast<unsigned>((1ull << (31 + l)) / div + 1);
+      shift = l - 1;
+    }
+  }
+  __device__ __forceinline__ unsigned div(unsigned n) const { return d == 1 ? n : __umulhi(n, m) >> shift; }
+};
+
 // ---------------------------------------------------------------------------------------------------
 // Small conversions
 // ---------------------------------------------------------------------------------------------------

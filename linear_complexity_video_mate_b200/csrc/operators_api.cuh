@@ -48,9 +48,9 @@ mate_status fill_qk(const mate_qk_config* c, const void* x, long long ldx, const
   p->tab_h = reinterpret_cast<const float2*>(th);
   p->tab_w = reinterpret_cast<const float2*>(tw);
   p->rows = (long long)c->B * c->T * c->H * c->W;
-  p->T = c->T;
-  p->H = c->H;
-  p->W = c->W;
+  p->n = FastDiv(c->T * c->H * c->W);
+  p->H = FastDiv(c->H);
+  p->W = FastDiv(c->W);
   p->hq = c->hq;
   p->hk = c->hk;
   p->hv = c->hv;
@@ -95,9 +95,10 @@ mate_status launch_qk(int kid, const mate_qk_config* c, QkParams p, cudaStream_t
   const long long warps = 16LL * device_sms();
   const int per = 32 / std::min(32, units > 16 ? 32 : units > 8 ? 16 : units > 4 ? 8 : 4);
   const int iters = std::max(ceil_div(c->hq, per), ceil_div(c->hk, per));
-  p.splits = static_cast<int>(std::max<long long>(1, std::min<long long>(iters, warps / p.rows)));
+  const int splits = static_cast<int>(std::max<long long>(1, std::min<long long>(iters, warps / p.rows)));
+  p.splits = FastDiv(splits);
   // the backward pass with as many blocks as are resident, so that their weight gradients are few
-  *blocks = static_cast<int>(std::min<long long>((p.rows * p.splits + kQkWarps - 1) / kQkWarps,
+  *blocks = static_cast<int>(std::min<long long>((p.rows * splits + kQkWarps - 1) / kQkWarps,
                                                  BWD ? std::min(kQkMaxParts, 2 * device_sms()) : 8 * device_sms()));
   trace_begin(kid, st);
   kernel<<<*blocks, kQkWarps * 32, 0, st>>>(p);

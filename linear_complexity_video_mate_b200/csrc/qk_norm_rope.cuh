@@ -28,13 +28,13 @@ struct QkParams {
   long long ldz;
   float* part;         // backward: per block [2][tp] partial weight gradients
   long long rows;
-  int T, H, W;
+  FastDiv n, H, W;     // tokens of a sample, H, W
   int hq, hk, hv, tp;
   int rt, rh, rw;
   int pairing;         // 0: channels 2i, 2i+1 of an axis block; 1: channels i, i + r/2
   float eps;
   int copy_v;
-  int splits;          // warps that share a row's heads
+  FastDiv splits;      // warps that share a row's heads
 };
 
 constexpr int kQkMaxDim = 256;
@@ -143,8 +143,9 @@ struct QkLane {
   }
 
   // The row's cos and sin of this lane's channels.
-  __device__ __forceinline__ void row(const QkParams& p, int tok) {
-    const int wi = tok % p.W, rest = tok / p.W, hi = rest % p.H, ti = rest / p.H;
+  __device__ __forceinline__ void row(const QkParams& p, unsigned row) {
+    const unsigned tok = row - p.n.div(row) * p.n.d, rest = p.W.div(tok), wi = tok - rest * p.W.d, ti = p.H.div(rest),
+                   hi = rest - ti * p.H.d;
     const float2* t0 = p.tab_t + (long long)ti * (p.rt / 2);
     const float2* t1 = p.tab_h + (long long)hi * (p.rh / 2);
     const float2* t2 = p.tab_w + (long long)wi * (p.rw / 2);
@@ -257,9 +258,9 @@ __device__ __forceinline__ float group_sum(float v, int G) {
 // Which of a row's heads a warp works on: unit -> row, part.
 struct QkUnit {
   int row, part;
-  __device__ __forceinline__ QkUnit(const QkParams& p, long long u) {
-    row = static_cast<int>(u / p.splits);
-    part = static_cast<int>(u - (long long)row * p.splits);
+  __device__ __forceinline__ QkUnit(const QkParams& p, unsigned u) {
+    row = static_cast<int>(p.splits.div(u));
+    part = static_cast<int>(u - row * p.splits.d);
   }
 };
 
@@ -267,7 +268,7 @@ struct QkUnit {
 template <typename T_>
 __device__ __forceinline__ void qk_copy_v(const QkParams& p, const T_* src, T_* dst, int part) {
   constexpr int V = 16 / sizeof(T_);
-  const int c0 = (p.hq + p.hk) * p.tp, nv = p.hv * p.tp / V, step = 32 * p.splits;
+  const int c0 = (p.hq + p.hk) * p.tp, nv = p.hv * p.tp / V, step = 32 * static_cast<int>(p.splits.d);
   const uint4* s = reinterpret_cast<const uint4*>(src + c0);
   uint4* d = reinterpret_cast<uint4*>(dst + c0);
   for (int v = part * 32 + (threadIdx.x & 31); v < nv; v += 4 * step) {
@@ -288,30 +289,31 @@ __global__ void __launch_bounds__(kQkWarps * 32, 2) qk_norm_rope_kernel(const Qk
   __shared__ float s_buf[MODE == kQkAny ? kQkWarps * 32 * NV * L::V : 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G;
   float* buf = s_buf + (MODE == kQkAny ? (warp * HPW + slot) * (G * NV * L::V) : 0);
-  const int n_tok = p.T * p.H * p.W;
+  const unsigned units = static_cast<unsigned>(p.rows) * p.splits.d;   // below 2^31: rows are shared only where they are few
+  const int splits = p.splits.d;
   const float inv_tp = 1.f / p.tp;
   L l;
   l.init(p, lane % G, G);
-  for (long long u = (long long)blockIdx.x * kQkWarps + warp; u < p.rows * p.splits; u += (long long)gridDim.x * kQkWarps) {
+  for (unsigned u = blockIdx.x * kQkWarps + warp; u < units; u += gridDim.x * kQkWarps) {
     const QkUnit un(p, u);
-    l.row(p, un.row % n_tok);
+    l.row(p, un.row);
     const T_* x = static_cast<const T_*>(p.x) + un.row * p.ldx;
     T_* out = static_cast<T_*>(p.out) + un.row * p.ldo;
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
       const int h0 = kind == 0 ? 0 : p.hq, h1 = kind == 0 ? p.hq : p.hq + p.hk;
-      for (int b = h0 + un.part * HPW + slot; b - slot < h1; b += UN * p.splits * HPW) {
+      for (int b = h0 + un.part * HPW + slot; b - slot < h1; b += UN * splits * HPW) {
         uint4 raw[UN][NV];
 #pragma unroll
         for (int j = 0; j < UN; ++j) {
-          const int head = b + j * p.splits * HPW;
+          const int head = b + j * splits * HPW;
 #pragma unroll
           for (int n = 0; n < NV; ++n)
             raw[j][n] = head < h1 && l.on[n] ? l.load(x + head * p.tp, n) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int j = 0; j < UN; ++j) {
-          const int head = b + j * p.splits * HPW;
+          const int head = b + j * splits * HPW;
           if (head - slot >= h1) break;   // the same for the warp
           float2 v[NV][L::P], ss = both(0.f);
 #pragma unroll
@@ -345,7 +347,8 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_bwd_kernel(const Q
   __shared__ float s_dw[kQkWarps][2][kQkMaxDim];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G;
   float* buf = s_buf + (MODE == kQkAny ? (warp * HPW + slot) * (G * NV * L::V) : 0);
-  const int n_tok = p.T * p.H * p.W;
+  const unsigned units = static_cast<unsigned>(p.rows) * p.splits.d;   // below 2^31: rows are shared only where they are few
+  const int splits = p.splits.d;
   const float inv_tp = 1.f / p.tp;
   L l;
   l.init(p, lane % G, G);
@@ -356,20 +359,20 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_bwd_kernel(const Q
     for (int n = 0; n < NV; ++n)
 #pragma unroll
       for (int k = 0; k < L::P; ++k) dw[q][n][k] = both(0.f);
-  for (long long u = (long long)blockIdx.x * kQkWarps + warp; u < p.rows * p.splits; u += (long long)gridDim.x * kQkWarps) {
+  for (unsigned u = blockIdx.x * kQkWarps + warp; u < units; u += gridDim.x * kQkWarps) {
     const QkUnit un(p, u);
-    l.row(p, un.row % n_tok);
+    l.row(p, un.row);
     const T_* x = static_cast<const T_*>(p.x) + un.row * p.ldx;
     const T_* dz = static_cast<const T_*>(p.dz) + un.row * p.ldz;
     T_* out = static_cast<T_*>(p.out) + un.row * p.ldo;
 #pragma unroll
     for (int kind = 0; kind < 2; ++kind) {
       const int h0 = kind == 0 ? 0 : p.hq, h1 = kind == 0 ? p.hq : p.hq + p.hk;
-      for (int b = h0 + un.part * HPW + slot; b - slot < h1; b += UN * p.splits * HPW) {
+      for (int b = h0 + un.part * HPW + slot; b - slot < h1; b += UN * splits * HPW) {
         uint4 raw[UN][NV], rawz[UN][NV];
 #pragma unroll
         for (int j = 0; j < UN; ++j) {
-          const int head = b + j * p.splits * HPW;
+          const int head = b + j * splits * HPW;
 #pragma unroll
           for (int n = 0; n < NV; ++n) {
             const bool ok = head < h1 && l.on[n];
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_bwd_kernel(const Q
         }
 #pragma unroll
         for (int j = 0; j < UN; ++j) {
-          const int head = b + j * p.splits * HPW;
+          const int head = b + j * splits * HPW;
           if (head - slot >= h1) break;
           float2 v[NV][L::P], g[NV][L::P], ss = both(0.f), gx = both(0.f);
 #pragma unroll
