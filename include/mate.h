@@ -458,7 +458,7 @@ MATE_API mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, 
  *   states    (null: not wanted) for the backward pass: mate_gated_scan_states_bytes(cfg) bytes, overwritten with
  *             the state before each run of rows
  * Requirements: D a multiple of 16 bytes of elements, B*T*H*W < 2^31.  ws: at least
- * mate_gated_scan_workspace_bytes(cfg) bytes; calls that overlap on the GPU need workspaces of their own.
+ * mate_gated_scan_workspace_bytes(cfg) bytes (0, and ws may be null, for short sequences); calls that overlap on the GPU need workspaces of their own.
  * States and gates are fp32; the result does not change from run to run.
  */
 typedef struct {

@@ -294,7 +294,7 @@ extern "C" {
 
 size_t mate_gated_scan_workspace_bytes(const mate_gated_scan_config* cfg) {
   if (check_gated(cfg) != MATE_OK) return 0;
-  return carve_gated(cfg, nullptr, false).total;
+  return gated_tiles(cfg) > 1 ? carve_gated(cfg, nullptr, false).total : 0;   // one tile of rows joins nothing
 }
 
 size_t mate_gated_scan_states_bytes(const mate_gated_scan_config* cfg) {
@@ -310,7 +310,7 @@ mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long lo
   MATE_TRY(fill_gated(cfg, x, ldx, g, ldg, bias, &p));
   const int es = cfg->dtype == MATE_BF16 ? 2 : 4;
   if (y == nullptr || y == x || y == g || !aligned16(y) || !row_stride_ok(ldy, cfg->D, es) || !aligned16(h0) ||
-      !aligned16(h_last) || !aligned16(states) || ws == nullptr || !aligned16(ws))
+      !aligned16(h_last) || !aligned16(states) || !aligned16(ws) || (ws == nullptr && gated_tiles(cfg) > 1))
     return MATE_ERR_ARG;
   if (ws_bytes < mate_gated_scan_workspace_bytes(cfg)) return MATE_ERR_WORKSPACE;
   p.h0 = h0;

@@ -9,6 +9,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import dataclasses
+import functools
 from typing import Dict, Optional
 
 import torch
@@ -338,23 +339,43 @@ def project_bf16(A: torch.Tensor, Wt: torch.Tensor, out: Optional[torch.Tensor] 
 
 # ------------------------------------------------------------------------------ operators beside the block
 # They take strided rows, tensors on any CUDA device (which need not be the current one) and an optional stream
-# of that device; what they allocate belongs to the stream they run on.
-def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
-    """Context in which `device` and `stream` are current (nothing to do where they already are)."""
+# of that device; what they allocate belongs to the stream they run on.  Devices go by their index here, and streams
+# by their raw handle: a call of few rows takes about as long on the host as on the GPU.
+_HERE = contextlib.nullcontext()
+
+
+def _on(index: int, stream: Optional[torch.cuda.Stream]):
+    """Context in which device `index` and `stream` are current (nothing to do where they already are)."""
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream on {stream.device}, tensors on {device}")
+        if stream.device.index != index:
+            raise ValueError(f"stream on {stream.device}, tensors on cuda:{index}")
         return torch.cuda.stream(stream)
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
 
 
-def _rows(t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int, device, name: str) -> int:
+def _raw_stream(index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
+def _device_index(device) -> int:
+    """Index of a CUDA device given as a name, an index or a torch.device."""
+    d = torch.device("cuda", device) if isinstance(device, int) else torch.device(device)
+    if d.type != "cuda":
+        raise ValueError(f"device {d}: a CUDA device is needed")
+    return torch.cuda.current_device() if d.index is None else d.index
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int, index: int, name: str) -> int:
     """Row stride in elements of a tensor that holds `rows` evenly strided rows of `cols` elements (of one row: any
-    stride that the library takes)."""
-    ok = t.is_cuda and t.dtype == dtype and t.dim() >= 1 and t.shape[-1] == cols and t.numel() == rows * cols and \
-        (t.stride(-1) == 1 or cols == 1) and (device is None or t.device == device)
-    ld, step = cols if rows != 1 else (cols + 15) // 16 * 16, None
+    stride that the library takes) on device `index`."""
+    ok = t.dtype is dtype and t.get_device() == index and index >= 0 and t.numel() == rows * cols and \
+        t.dim() >= 1 and t.shape[-1] == cols
+    ld = cols if rows != 1 else (cols + 15) // 16 * 16
+    if ok and t.is_contiguous():
+        return ld
+    ok = ok and (t.stride(-1) == 1 or cols == 1)
     if ok:
+        step = None
         for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
             if size == 1:
                 continue
@@ -363,28 +384,28 @@ def _rows(t: torch.Tensor, dtype: torch.dtype, rows: int, cols: int, device, nam
             ok = ok and st == step
             step *= size
     if not ok:
-        raise ValueError(f"{name}: expected {rows} evenly strided rows of {cols} {dtype} elements"
-                         f"{'' if device is None else f' on {device}'}, got {t.dtype} {tuple(t.shape)} with strides "
-                         f"{t.stride()} on {t.device}")
+        raise ValueError(f"{name}: expected {rows} evenly strided rows of {cols} {dtype} elements on "
+                         f"{'a CUDA device' if index < 0 else f'cuda:{index}'}, got {t.dtype} {tuple(t.shape)} with "
+                         f"strides {t.stride()} on {t.device}")
     return ld
 
 
-def _flat(t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, device, name: str):
-    """Pointer of an optional contiguous tensor on `device`."""
+def _flat(t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, index: int, name: str) -> Optional[int]:
+    """Address of an optional contiguous tensor on device `index`."""
     if t is None:
         return None
-    _need(t, dtype, numel, name)
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the other tensors on {device}")
-    return _p(t)
+    if t.dtype is not dtype or t.get_device() != index or t.numel() != numel or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor with {numel} elements on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _workspace(ws: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
-    """The caller's workspace (uint8, checked), else a new one of the current stream."""
+def _workspace(ws: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> Optional[torch.Tensor]:
+    """The caller's workspace (uint8, checked), else a new one of the current stream; None where none is needed."""
     if ws is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if not ws.is_cuda or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != device or ws.numel() < nbytes:
-        raise ValueError(f"ws: expected at least {nbytes} contiguous uint8 elements on {device}, got {ws.dtype} "
+        return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous() or ws.device != like.device or ws.numel() < nbytes:
+        raise ValueError(f"ws: expected at least {nbytes} contiguous uint8 elements on {like.device}, got {ws.dtype} "
                          f"{tuple(ws.shape)} on {ws.device}")
     return ws
 
@@ -396,6 +417,12 @@ def _ints(obj, names):
         if not -(1 << 31) <= v < (1 << 31):
             raise ValueError(f"{k} = {v} does not fit a 32-bit int")
     return vals
+
+
+def _keep(obj, **values):
+    """Derived values of a frozen configuration."""
+    for k, v in values.items():
+        object.__setattr__(obj, k, v)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -425,34 +452,33 @@ class QkConfig:
         c = _lib.CQkConfig(*_ints(self, ("B", "T", "H", "W", "hq", "hk", "hv", "tp", "rt", "rh", "rw")),
                            int(self.pairing == "halves"), self.eps,
                            _lib.MATE_BF16 if self.dtype == "bf16" else _lib.MATE_F32)
-        object.__setattr__(self, "ccfg", c)
+        _keep(self, ccfg=c, ref=ctypes.byref(c), tdtype=torch_dtype(self), rows=self.B * self.T * self.H * self.W,
+              width=(self.hq + self.hk + self.hv) * self.tp)
 
-    @property
-    def rows(self) -> int:
-        return self.B * self.T * self.H * self.W
-
-    @property
-    def width(self) -> int:
-        return (self.hq + self.hk + self.hv) * self.tp
+    @functools.cached_property
+    def backward_workspace_bytes(self) -> int:
+        return _lib.load().mate_qk_norm_rope_backward_workspace_bytes(self.ref)
 
 
 def rope_table(count: int, dims: int, start: int = 0, theta: float = 10000.0, device="cuda",
                stream=None) -> torch.Tensor:
     """[count, dims / 2, 2] fp32: (cos, sin) of (start + p) theta^(-2 i / dims), the angle in 64 bits (made once)."""
-    device = torch.empty(0, device=device).device
-    with _on(device, stream):
-        tab = torch.empty((max(int(count), 0), max(int(dims), 0) // 2, 2), dtype=torch.float32, device=device)
-        if dims != 0:
-            _lib.check(_lib.load().mate_rope_table(_p(tab), int(start), int(count), int(dims), float(theta), _s(None)),
-                       "mate_rope_table")
+    index = _device_index(device)
+    with _on(index, stream):
+        tab = torch.empty((max(int(count), 0), max(int(dims), 0) // 2, 2), dtype=torch.float32, device=f"cuda:{index}")
+        st = 0 if dims == 0 else _lib.load().mate_rope_table(tab.data_ptr(), int(start), int(count), int(dims),
+                                                             float(theta), _raw_stream(index))
+    _lib.check(st, "mate_rope_table")
     return tab
 
 
-def _qk_tables(tables, cfg: QkConfig, device):
+def _qk_tables(tables, cfg: QkConfig, index: int):
     if len(tables) != 3:
         raise ValueError(f"tables: expected the t, h and w tables, got {len(tables)}")
-    return [None if r == 0 else _flat(t, torch.float32, n * r, device, f"{ax} table")
-            for t, n, r, ax in zip(tables, (cfg.T, cfg.H, cfg.W), (cfg.rt, cfg.rh, cfg.rw), "thw")]
+    t, h, w = tables
+    return (_flat(t, torch.float32, cfg.T * cfg.rt, index, "t table") if cfg.rt else None,
+            _flat(h, torch.float32, cfg.H * cfg.rh, index, "h table") if cfg.rh else None,
+            _flat(w, torch.float32, cfg.W * cfg.rw, index, "w table") if cfg.rw else None)
 
 
 def qk_norm_rope(qkv: torch.Tensor, wq: Optional[torch.Tensor], wk: Optional[torch.Tensor], tables, cfg: QkConfig,
@@ -460,15 +486,17 @@ def qk_norm_rope(qkv: torch.Tensor, wq: Optional[torch.Tensor], wk: Optional[tor
     """RMS norm of every query and key head (weights wq, wk [tp] fp32 or None) and rotation by the token's position,
     on packed q | k | v rows; value columns pass.  tables: the (t, h, w) tables of rope_table (None for an axis with no
     channels).  out=qkv works in place."""
-    dt, dev = torch_dtype(cfg), qkv.device
-    ldi = _rows(qkv, dt, cfg.rows, cfg.width, None, "qkv")
-    with _on(dev, stream):
+    dt, index = cfg.tdtype, qkv.get_device()
+    ldi = _rows(qkv, dt, cfg.rows, cfg.width, index, "qkv")
+    tabs = _qk_tables(tables, cfg, index)
+    with _on(index, stream):
         if out is None:
-            out = torch.empty(qkv.shape, dtype=dt, device=dev)
-        ldo = _rows(out, dt, cfg.rows, cfg.width, dev, "out")
+            out, ldo = torch.empty_like(qkv, memory_format=torch.contiguous_format), cfg.width
+        else:
+            ldo = _rows(out, dt, cfg.rows, cfg.width, index, "out") if out is not qkv else ldi
         st = _lib.load().mate_qk_norm_rope(
-            _p(qkv), ldi, _flat(wq, torch.float32, cfg.tp, dev, "wq"), _flat(wk, torch.float32, cfg.tp, dev, "wk"),
-            *_qk_tables(tables, cfg, dev), _p(out), ldo, ctypes.byref(cfg.ccfg), _s(None))
+            qkv.data_ptr(), ldi, _flat(wq, torch.float32, cfg.tp, index, "wq"),
+            _flat(wk, torch.float32, cfg.tp, index, "wk"), *tabs, out.data_ptr(), ldo, cfg.ref, _raw_stream(index))
     _lib.check(st, "mate_qk_norm_rope")
     return out
 
@@ -478,21 +506,23 @@ def qk_norm_rope_backward(qkv: torch.Tensor, wq: Optional[torch.Tensor], wk: Opt
                           stream=None) -> Dict[str, torch.Tensor]:
     """Gradients of qk_norm_rope from its input and the output gradient: dqkv (may be dout or qkv itself), dwq and dwk
     [tp] fp32 (summed over rows and heads in a fixed order)."""
-    lib, dt, dev = _lib.load(), torch_dtype(cfg), qkv.device
-    ldi = _rows(qkv, dt, cfg.rows, cfg.width, None, "qkv")
-    ldg = _rows(dout, dt, cfg.rows, cfg.width, dev, "dout")
-    with _on(dev, stream):
+    dt, index = cfg.tdtype, qkv.get_device()
+    ldi = _rows(qkv, dt, cfg.rows, cfg.width, index, "qkv")
+    ldg = _rows(dout, dt, cfg.rows, cfg.width, index, "dout")
+    tabs = _qk_tables(tables, cfg, index)
+    with _on(index, stream):
         if dqkv is None:
-            dqkv = torch.empty(qkv.shape, dtype=dt, device=dev)
-        ldd = _rows(dqkv, dt, cfg.rows, cfg.width, dev, "dqkv")
-        dwq = torch.empty(cfg.tp, dtype=torch.float32, device=dev)
-        dwk = torch.empty(cfg.tp, dtype=torch.float32, device=dev)
-        nb = lib.mate_qk_norm_rope_backward_workspace_bytes(ctypes.byref(cfg.ccfg))
-        ws = _workspace(ws, nb, dev)
-        st = lib.mate_qk_norm_rope_backward(
-            _p(qkv), ldi, _flat(wq, torch.float32, cfg.tp, dev, "wq"), _flat(wk, torch.float32, cfg.tp, dev, "wk"),
-            *_qk_tables(tables, cfg, dev), _p(dout), ldg, _p(dqkv), ldd, _p(dwq), _p(dwk), ctypes.byref(cfg.ccfg), _p(ws),
-            ws.numel(), _s(None))
+            dqkv = torch.empty_like(qkv, memory_format=torch.contiguous_format)
+        ldd = _rows(dqkv, dt, cfg.rows, cfg.width, index, "dqkv")
+        dwq = torch.empty(cfg.tp, dtype=torch.float32, device=qkv.device)
+        dwk = torch.empty(cfg.tp, dtype=torch.float32, device=qkv.device)
+        ws = _workspace(ws, cfg.backward_workspace_bytes, qkv)
+        if ws is None:
+            raise ValueError(f"qk_norm_rope_backward: {cfg} is not supported")
+        st = _lib.load().mate_qk_norm_rope_backward(
+            qkv.data_ptr(), ldi, _flat(wq, torch.float32, cfg.tp, index, "wq"),
+            _flat(wk, torch.float32, cfg.tp, index, "wk"), *tabs, dout.data_ptr(), ldg, dqkv.data_ptr(), ldd,
+            dwq.data_ptr(), dwk.data_ptr(), cfg.ref, ws.data_ptr(), ws.numel(), _raw_stream(index))
     _lib.check(st, "mate_qk_norm_rope_backward")
     return dict(dqkv=dqkv, dwq=dwq, dwk=dwk)
 
@@ -516,21 +546,28 @@ class GatedScanConfig:
             raise ValueError(f"dtype {self.dtype!r} (bf16, f32)")
         c = _lib.CGatedScanConfig(*_ints(self, ("B", "T", "H", "W", "D", "order")), int(bool(self.reverse)),
                                   _lib.MATE_BF16 if self.dtype == "bf16" else _lib.MATE_F32)
-        object.__setattr__(self, "ccfg", c)
+        _keep(self, ccfg=c, ref=ctypes.byref(c), tdtype=torch_dtype(self), rows=self.B * self.T * self.H * self.W)
 
-    @property
-    def rows(self) -> int:
-        return self.B * self.T * self.H * self.W
+    @functools.cached_property
+    def workspace_bytes(self) -> int:
+        return _lib.load().mate_gated_scan_workspace_bytes(self.ref)
+
+    @functools.cached_property
+    def backward_workspace_bytes(self) -> int:
+        return _lib.load().mate_gated_scan_backward_workspace_bytes(self.ref)
+
+    @functools.cached_property
+    def states_numel(self) -> int:
+        return _lib.load().mate_gated_scan_states_bytes(self.ref) // 4
 
 
 def gated_scan_states(cfg: GatedScanConfig, device="cuda", stream=None) -> torch.Tensor:
     """Buffer (fp32) for the states that gated_scan leaves for gated_scan_backward."""
-    device = torch.empty(0, device=device).device
-    nb = _lib.load().mate_gated_scan_states_bytes(ctypes.byref(cfg.ccfg))
-    if nb == 0:
+    index = _device_index(device)
+    if cfg.states_numel == 0:
         raise ValueError(f"gated_scan_states: {cfg} is not supported")
-    with _on(device, stream):
-        return torch.empty(nb // 4, dtype=torch.float32, device=device)
+    with _on(index, stream):
+        return torch.empty(cfg.states_numel, dtype=torch.float32, device=f"cuda:{index}")
 
 
 def gated_scan(x: torch.Tensor, g: torch.Tensor, cfg: GatedScanConfig, bias: Optional[torch.Tensor] = None,
@@ -539,23 +576,22 @@ def gated_scan(x: torch.Tensor, g: torch.Tensor, cfg: GatedScanConfig, bias: Opt
     """h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(g + bias), along the grid's scan order: (y, h_last).
     x, g: rows of D channels in grid order (strided rows allowed); bias [D], h0 and h_last [B, D] fp32.
     states (gated_scan_states): filled for gated_scan_backward."""
-    lib, dt, dev = _lib.load(), torch_dtype(cfg), x.device
-    ldx = _rows(x, dt, cfg.rows, cfg.D, None, "x")
-    ldg = _rows(g, dt, cfg.rows, cfg.D, dev, "g")
-    with _on(dev, stream):
+    dt, f32, index, rows, D = cfg.tdtype, torch.float32, x.get_device(), cfg.rows, cfg.D
+    ldx = _rows(x, dt, rows, D, index, "x")
+    ldg = _rows(g, dt, rows, D, index, "g")
+    with _on(index, stream):
         if y is None:
-            y = torch.empty(x.shape, dtype=dt, device=dev)
+            y, ldy = torch.empty_like(x, memory_format=torch.contiguous_format), D
+        else:
+            ldy = _rows(y, dt, rows, D, index, "y")
         if h_last is None:
-            h_last = torch.empty((cfg.B, cfg.D), dtype=torch.float32, device=dev)
-        ldy = _rows(y, dt, cfg.rows, cfg.D, dev, "y")
-        if states is not None:
-            nb = lib.mate_gated_scan_states_bytes(ctypes.byref(cfg.ccfg))
-            _flat(states, torch.float32, nb // 4, dev, "states")
-        ws = _workspace(ws, lib.mate_gated_scan_workspace_bytes(ctypes.byref(cfg.ccfg)), dev)
-        st = lib.mate_gated_scan(_p(x), ldx, _p(g), ldg, _flat(bias, torch.float32, cfg.D, dev, "bias"),
-                                 _flat(h0, torch.float32, cfg.B * cfg.D, dev, "h0"), _p(y), ldy,
-                                 _flat(h_last, torch.float32, cfg.B * cfg.D, dev, "h_last"), _p(states),
-                                 ctypes.byref(cfg.ccfg), _p(ws), ws.numel(), _s(None))
+            h_last = torch.empty((cfg.B, D), dtype=f32, device=x.device)
+        ws = _workspace(ws, cfg.workspace_bytes, x)
+        st = _lib.load().mate_gated_scan(
+            x.data_ptr(), ldx, g.data_ptr(), ldg, _flat(bias, f32, D, index, "bias"),
+            _flat(h0, f32, cfg.B * D, index, "h0"), y.data_ptr(), ldy, _flat(h_last, f32, cfg.B * D, index, "h_last"),
+            None if states is None else _flat(states, f32, cfg.states_numel, index, "states"), cfg.ref,
+            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _raw_stream(index))
     _lib.check(st, "mate_gated_scan")
     return y, h_last
 
@@ -566,24 +602,28 @@ def gated_scan_backward(x: torch.Tensor, g: torch.Tensor, states: torch.Tensor, 
                         stream=None) -> Dict[str, torch.Tensor]:
     """Gradients of gated_scan from its inputs, the states it left and the gradients dy of y and dh_last of h_last
     (None: zero): dx, dg, dh0 [B, D] and, with a bias, dbias [D]."""
-    lib, dt, dev = _lib.load(), torch_dtype(cfg), x.device
-    ldx = _rows(x, dt, cfg.rows, cfg.D, None, "x")
-    ldg = _rows(g, dt, cfg.rows, cfg.D, dev, "g")
-    lddy = _rows(dy, dt, cfg.rows, cfg.D, dev, "dy")
-    with _on(dev, stream):
-        dx = torch.empty(x.shape, dtype=dt, device=dev) if dx is None else dx
-        dg = torch.empty(g.shape, dtype=dt, device=dev) if dg is None else dg
-        grads = dict(dx=dx, dg=dg, dh0=torch.empty((cfg.B, cfg.D), dtype=torch.float32, device=dev))
+    dt, f32, index, rows, D = cfg.tdtype, torch.float32, x.get_device(), cfg.rows, cfg.D
+    ldx = _rows(x, dt, rows, D, index, "x")
+    ldg = _rows(g, dt, rows, D, index, "g")
+    lddy = _rows(dy, dt, rows, D, index, "dy")
+    with _on(index, stream):
+        if dx is None:
+            dx = torch.empty_like(x, memory_format=torch.contiguous_format)
+        if dg is None:
+            dg = torch.empty_like(g, memory_format=torch.contiguous_format)
+        grads = dict(dx=dx, dg=dg, dh0=torch.empty((cfg.B, D), dtype=f32, device=x.device))
+        dbias = None
         if bias is not None:
-            grads["dbias"] = torch.empty(cfg.D, dtype=torch.float32, device=dev)
-        nb = lib.mate_gated_scan_states_bytes(ctypes.byref(cfg.ccfg))
-        ws = _workspace(ws, lib.mate_gated_scan_backward_workspace_bytes(ctypes.byref(cfg.ccfg)), dev)
-        st = lib.mate_gated_scan_backward(
-            _p(x), ldx, _p(g), ldg, _flat(bias, torch.float32, cfg.D, dev, "bias"),
-            _flat(states, torch.float32, nb // 4, dev, "states"), _p(dy), lddy,
-            _flat(dh_last, torch.float32, cfg.B * cfg.D, dev, "dh_last"), _p(dx), _rows(dx, dt, cfg.rows, cfg.D, dev, "dx"),
-            _p(dg), _rows(dg, dt, cfg.rows, cfg.D, dev, "dg"), _p(grads.get("dbias")), _p(grads["dh0"]),
-            ctypes.byref(cfg.ccfg), _p(ws), ws.numel(), _s(None))
+            dbias = grads["dbias"] = torch.empty(D, dtype=f32, device=x.device)
+        ws = _workspace(ws, cfg.backward_workspace_bytes, x)
+        if ws is None:
+            raise ValueError(f"gated_scan_backward: {cfg} is not supported")
+        st = _lib.load().mate_gated_scan_backward(
+            x.data_ptr(), ldx, g.data_ptr(), ldg, _flat(bias, f32, D, index, "bias"),
+            _flat(states, f32, cfg.states_numel, index, "states"), dy.data_ptr(), lddy,
+            _flat(dh_last, f32, cfg.B * D, index, "dh_last"), dx.data_ptr(), _rows(dx, dt, rows, D, index, "dx"),
+            dg.data_ptr(), _rows(dg, dt, rows, D, index, "dg"), None if dbias is None else dbias.data_ptr(),
+            grads["dh0"].data_ptr(), cfg.ref, ws.data_ptr(), ws.numel(), _raw_stream(index))
     _lib.check(st, "mate_gated_scan_backward")
     return grads
 
@@ -599,18 +639,19 @@ def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Opti
     q = x / scale to the nearest integer, ties to even.  A new q has its rows padded to a multiple of 16 bytes."""
     if x.dim() != 2:
         raise ValueError(f"x: expected [M, K], got {tuple(x.shape)}")
-    (M, K), dev, code = x.shape, x.device, _mate_dtype(x.dtype, "x")
-    ldx = _rows(x, x.dtype, M, K, None, "x")
-    with _on(dev, stream):
+    (M, K), index, code = x.shape, x.get_device(), _mate_dtype(x.dtype, "x")
+    ldx = _rows(x, x.dtype, M, K, index, "x")
+    with _on(index, stream):
         if q is None:
             ldq = (K + 15) // 16 * 16
-            q = torch.empty((M, ldq), dtype=torch.int8, device=dev)
+            q = torch.empty((M, ldq), dtype=torch.int8, device=x.device)
             q = q if ldq == K else q[:, :K]
+        else:
+            ldq = _rows(q, torch.int8, M, K, index, "q")
         if scale is None:
-            scale = torch.empty(M, dtype=torch.float32, device=dev)
-        ldq = _rows(q, torch.int8, M, K, dev, "q")
-        st = _lib.load().mate_quantize_rows(_p(x), ldx, M, K, code, _p(q), ldq,
-                                            _flat(scale, torch.float32, M, dev, "scale"), _s(None)) if M else 0
+            scale = torch.empty(M, dtype=torch.float32, device=x.device)
+        st = _lib.load().mate_quantize_rows(x.data_ptr(), ldx, M, K, code, q.data_ptr(), ldq,
+                                            _flat(scale, torch.float32, M, index, "scale"), _raw_stream(index)) if M else 0
     _lib.check(st, "mate_quantize_rows")
     return q, scale
 
@@ -622,18 +663,18 @@ def project_int8(A: torch.Tensor, a_scale: torch.Tensor, Wt: torch.Tensor, w_sca
     a_scale [M], w_scale [N], bias [N] fp32 -> C [M, N] bf16 or fp32.  The integer sums are exact."""
     if A.dim() != 2 or Wt.dim() != 2:
         raise ValueError(f"A and Wt: expected [M, K] and [N, K], got {tuple(A.shape)} and {tuple(Wt.shape)}")
-    (M, K), N, dev = A.shape, Wt.shape[0], A.device
-    lda = _rows(A, torch.int8, M, K, None, "A")
-    ldw = _rows(Wt, torch.int8, N, K, dev, "Wt")
-    with _on(dev, stream):
+    (M, K), N, index, f32 = A.shape, Wt.shape[0], A.get_device(), torch.float32
+    lda = _rows(A, torch.int8, M, K, index, "A")
+    ldw = _rows(Wt, torch.int8, N, K, index, "Wt")
+    with _on(index, stream):
         if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=dev)
-        code = _mate_dtype(out.dtype, "out")
-        ldc = _rows(out, out.dtype, M, N, dev, "out")
+            code, out, ldc = _mate_dtype(out_dtype, "out_dtype"), torch.empty((M, N), dtype=out_dtype, device=A.device), N
+        else:
+            code, ldc = _mate_dtype(out.dtype, "out"), _rows(out, out.dtype, M, N, index, "out")
         st = _lib.load().mate_project_int8(
-            _p(A), lda, _flat(a_scale, torch.float32, M, dev, "a_scale"), M, K, _p(Wt), ldw,
-            _flat(w_scale, torch.float32, N, dev, "w_scale"), N, _flat(bias, torch.float32, N, dev, "bias"), _p(out), ldc,
-            code, _s(None)) if M else 0
+            A.data_ptr(), lda, _flat(a_scale, f32, M, index, "a_scale"), M, K, Wt.data_ptr(), ldw,
+            _flat(w_scale, f32, N, index, "w_scale"), N, _flat(bias, f32, N, index, "bias"), out.data_ptr(), ldc, code,
+            _raw_stream(index)) if M else 0
     _lib.check(st, "mate_project_int8")
     return out
 
