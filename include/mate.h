@@ -564,11 +564,13 @@ typedef enum {
   MATE_K_QK_NORM_ROPE = 28,    /* mate_qk_norm_rope */
   MATE_K_QK_NORM_ROPE_BWD = 29, /* mate_qk_norm_rope_backward: dqkv and partial weight gradients */
   MATE_K_QK_WEIGHT_GRAD = 30,  /* mate_qk_norm_rope_backward: sum of the partial weight gradients */
-  MATE_K_GATED_SCAN = 31,      /* mate_gated_scan */
+  MATE_K_GATED_SCAN = 31,      /* mate_gated_scan: the rows */
   MATE_K_GATED_SCAN_BWD = 32,  /* mate_gated_scan_backward */
   MATE_K_QUANTIZE_ROWS = 33,   /* mate_quantize_rows */
   MATE_K_PROJECT_INT8 = 34,    /* mate_project_int8 */
-  MATE_K_GATED_SCAN_BIAS = 35  /* mate_gated_scan_backward: sum of the partial bias gradients */
+  MATE_K_GATED_SCAN_BIAS = 35, /* mate_gated_scan_backward: sum of the partial bias gradients */
+  MATE_K_GATED_SCAN_PAIRS = 36, /* mate_gated_scan and its backward: what each chunk of rows does to the state */
+  MATE_K_GATED_SCAN_CARRY = 37 /* mate_gated_scan and its backward: the state at each chunk */
 } mate_kernel;
 
 typedef struct {

@@ -1547,6 +1547,8 @@ const char* mate_kernel_name(int kernel) {
     case MATE_K_QK_WEIGHT_GRAD: return "qk_weight_grad";
     case MATE_K_GATED_SCAN: return "gated_scan";
     case MATE_K_GATED_SCAN_BWD: return "gated_scan_backward";
+    case MATE_K_GATED_SCAN_PAIRS: return "gated_scan_pairs";
+    case MATE_K_GATED_SCAN_CARRY: return "gated_scan_carry";
     case MATE_K_GATED_SCAN_BIAS: return "gated_scan_bias";
     case MATE_K_QUANTIZE_ROWS: return "quantize_rows";
     case MATE_K_PROJECT_INT8: return "project_int8";

@@ -184,6 +184,18 @@ mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, const flo
 // ------------------------------------------------------------------------------ gated scan
 namespace {
 
+// Rows per chunk: long chunks carry little, but there have to be threads enough (four channels of a chunk each) to fill
+// the SMs.
+int gated_chunk(const mate_gated_scan_config* c) {
+  const long long n = (long long)c->T * c->H * c->W, cols = (long long)c->B * (c->D / 4);
+  if (n <= kGsOneChunk) return static_cast<int>(n);
+  int r = kGsMaxChunk;
+  while (r > 16 && (n + r - 1) / r * cols < 1024LL * 148) r /= 2;
+  return r;
+}
+
+int gated_chunks(const mate_gated_scan_config* c) { return ceil_div((long long)c->T * c->H * c->W, gated_chunk(c)); }
+
 mate_status check_gated(const mate_gated_scan_config* c) {
   if (c == nullptr) return MATE_ERR_ARG;
   if (c->dtype != MATE_BF16 && c->dtype != MATE_F32) return MATE_ERR_ARG;
@@ -192,14 +204,35 @@ mate_status check_gated(const mate_gated_scan_config* c) {
   if (c->D % (c->dtype == MATE_BF16 ? 8 : 4)) return MATE_ERR_SHAPE;
   const long long hw = (long long)c->H * c->W;
   if (hw >= (1LL << 31) || hw * c->T >= (1LL << 31) || hw * c->T * c->B >= (1LL << 31)) return MATE_ERR_SHAPE;
-  // tiles are counted in 31 bits (a block looks one ticket ahead)
-  const long long tiles = (long long)ceil_div(hw * c->T, kGsRows<float>) * c->B;
-  if (tiles * ceil_div(c->D, kGsChan) >= (1LL << 31)) return MATE_ERR_SHAPE;
+  // threads of two channels of a chunk, and columns of all samples, are counted in 31 bits
+  if ((long long)c->B * c->D >= (1LL << 31) || (long long)gated_chunks(c) * c->B >= (1LL << 31) / (c->D / 2))
+    return MATE_ERR_SHAPE;
   return MATE_OK;
 }
 
-int gated_tiles(const mate_gated_scan_config* c) {
-  return ceil_div((long long)c->T * c->H * c->W, c->dtype == MATE_BF16 ? kGsRows<__nv_bfloat16> : kGsRows<float>);
+// The grid rows along scan order `order` (fastest axis first), `reverse`: from the last position.
+GsOrder gated_order(const mate_gated_scan_config* c, int reverse) {
+  const int H = c->H, W = c->W, T = c->T, n = T * H * W;
+  int dim[3], step[3];
+  switch (c->order) {
+    case 0: dim[0] = n, dim[1] = dim[2] = 1, step[0] = 1, step[1] = step[2] = 0; break;
+    case 1: dim[0] = H, dim[1] = W, dim[2] = T, step[0] = W, step[1] = 1, step[2] = H * W; break;
+    case 2: dim[0] = T, dim[1] = W, dim[2] = H, step[0] = H * W, step[1] = 1, step[2] = W; break;
+    default: dim[0] = T, dim[1] = H, dim[2] = W, step[0] = H * W, step[1] = W, step[2] = 1; break;
+  }
+  GsOrder o;
+  o.base = 0;
+  if (reverse)
+    for (int i = 0; i < 3; ++i) {
+      o.base += (dim[i] - 1) * step[i];
+      step[i] = -step[i];
+    }
+  o.n0 = FastDiv(dim[0]);
+  o.n1 = FastDiv(dim[1]);
+  o.s0 = step[0];
+  o.d1 = step[1] - dim[0] * step[0];
+  o.d2 = step[2] - dim[1] * step[1];
+  return o;
 }
 
 mate_status fill_gated(const mate_gated_scan_config* c, const void* x, long long ldx, const void* g, long long ldg,
@@ -210,80 +243,53 @@ mate_status fill_gated(const mate_gated_scan_config* c, const void* x, long long
     return MATE_ERR_ARG;
   p->x = x;
   p->g = g;
-  p->ldx = ldx;
-  p->ldg = ldg;
+  p->ldx = static_cast<unsigned>(ldx);
+  p->ldg = static_cast<unsigned>(ldg);
   p->bias = bias;
-  p->B = c->B;
-  p->T = c->T;
-  p->H = c->H;
-  p->W = c->W;
+  p->order = gated_order(c, c->reverse);
+  p->back = gated_order(c, !c->reverse);
+  p->B = FastDiv(c->B);
   p->D = c->D;
-  p->order = c->order;
-  p->reverse = c->reverse;
   p->n = c->T * c->H * c->W;
-  p->tiles = gated_tiles(c);
-  p->cblocks = ceil_div(c->D, kGsChan);
+  p->chunk = gated_chunk(c);
+  p->chunks = gated_chunks(c);
+  p->states_per = ceil_div(p->n, kGsState);
   return MATE_OK;
 }
 
 struct GatedScanScratch {
-  unsigned* sync;             // the ticket counter and the abort word
-  unsigned long long *pair, *group;
-  size_t bytes;               // of all that a call fills with ones first
+  float2* pair;
+  float* carry;
   float* dbias_part;
-  size_t total;
+  size_t bytes;
 };
 
-// A sequence of one tile joins nothing and needs no scratch but the partial bias sums.
+// A sequence of one chunk joins nothing.
 GatedScanScratch carve_gated(const mate_gated_scan_config* c, void* ws, bool backward) {
   GatedScanScratch s{};
   Carver cv{static_cast<char*>(ws)};
-  const size_t tiles = gated_tiles(c), row = (size_t)c->B * c->D;
-  s.sync = cv.take<unsigned>(64);
-  if (tiles > 1) {
-    s.pair = cv.take<unsigned long long>((tiles - 1) * row);
-    s.group = cv.take<unsigned long long>(((tiles - 1) / kGsGroup + 1) * row);
+  const size_t chunks = gated_chunks(c), cols = (size_t)c->B * c->D;
+  if (chunks > 1) {
+    s.pair = cv.take<float2>(chunks * cols);
+    s.carry = cv.take<float>(chunks * cols);
   }
+  if (backward) s.dbias_part = cv.take<float>(chunks * cols);
   s.bytes = cv.off;
-  if (backward) s.dbias_part = cv.take<float>(tiles * row);
-  s.total = cv.off + 256;
   return s;
 }
 
-// Rows of 128 bytes' worth of channels for the gathers (rows are picked one by one; behind the matrix zeros).
-bool make_tmap_rows(CUtensorMap* m, const void* ptr, long long rows, int cols, long long ld, bool bf16) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const int es = bf16 ? 2 : 4;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), 1};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(ptr), dims,
-            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+// Grid of a kernel whose threads take 2 np channels of a chunk.
+int gated_blocks(GatedScanParams* p, int np) {
+  p->per = FastDiv(p->D / (2 * np));
+  p->threads = static_cast<unsigned>(p->chunks) * p->B.d * p->per.d;
+  return static_cast<int>((p->threads + 255u) / 256u);
 }
 
-// Launches a scan kernel over all tiles, after filling the scratch that the tiles publish in.
-mate_status launch_gated(void (*kernel)(GsMaps, GatedScanParams), int kid, size_t smem, GatedScanParams p, bool bf16,
-                         const GatedScanScratch& s, void* ws, cudaStream_t st) {
-  if (p.tiles > 1) {
-    if (!cuda_ok(cudaMemsetAsync(ws, 0xff, s.bytes, st))) return MATE_ERR_CUDA;
-    p.ticket = s.sync;
-    p.abort = s.sync + 32;
-    p.pair = s.pair;
-    p.group = s.group;
-  }
-  GsMaps maps;
-  const long long rows = (long long)p.B * p.n;
-  if (!make_tmap_rows(&maps.x, p.x, rows, p.D, p.ldx, bf16) || !make_tmap_rows(&maps.g, p.g, rows, p.D, p.ldg, bf16) ||
-      (p.dy != nullptr && !make_tmap_rows(&maps.dy, p.dy, rows, p.D, p.lddy, bf16)))
-    return MATE_ERR_CUDA;
-  if (p.dy == nullptr) maps.dy = maps.x;   // never read
-  if (!set_smem(kernel, smem)) return MATE_ERR_CUDA;
-  const long long total = (long long)p.tiles * p.B * p.cblocks;
-  trace_begin(kid, st);
-  kernel<<<static_cast<int>(std::min<long long>(total, 2LL * device_sms())), kGsThreads, smem, st>>>(maps, p);
+mate_status launch_carry(const GatedScanParams& p, const float* start, int back, cudaStream_t st) {
+  const int cols = static_cast<int>(p.B.d) * p.D;
+  trace_begin(MATE_K_GATED_SCAN_CARRY, st);
+  gated_carry_kernel<<<ceil_div(cols, kGsCarryCh), kGsCarryCh * kGsCarrySeg, 0, st>>>(p.pair, start, p.carry, p.chunks,
+                                                                                      cols, back);
   MATE_LAUNCH_CHECK();
   return MATE_OK;
 }
@@ -294,12 +300,12 @@ extern "C" {
 
 size_t mate_gated_scan_workspace_bytes(const mate_gated_scan_config* cfg) {
   if (check_gated(cfg) != MATE_OK) return 0;
-  return gated_tiles(cfg) > 1 ? carve_gated(cfg, nullptr, false).total : 0;   // one tile of rows joins nothing
+  return carve_gated(cfg, nullptr, false).bytes;
 }
 
 size_t mate_gated_scan_states_bytes(const mate_gated_scan_config* cfg) {
   if (check_gated(cfg) != MATE_OK) return 0;
-  return (size_t)cfg->B * gated_tiles(cfg) * cfg->D * sizeof(float);
+  return (size_t)cfg->B * ceil_div((long long)cfg->T * cfg->H * cfg->W, kGsState) * cfg->D * sizeof(float);
 }
 
 mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long long ldg, const float* bias,
@@ -308,36 +314,40 @@ mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long lo
   MATE_TRY(check_gated(cfg));
   GatedScanParams p{};
   MATE_TRY(fill_gated(cfg, x, ldx, g, ldg, bias, &p));
-  const int es = cfg->dtype == MATE_BF16 ? 2 : 4;
-  if (y == nullptr || y == x || y == g || !aligned16(y) || !row_stride_ok(ldy, cfg->D, es) || !aligned16(h0) ||
-      !aligned16(h_last) || !aligned16(states) || !aligned16(ws) || (ws == nullptr && gated_tiles(cfg) > 1))
+  const bool bf = cfg->dtype == MATE_BF16;
+  const size_t need = mate_gated_scan_workspace_bytes(cfg);
+  if (y == nullptr || y == x || y == g || !aligned16(y) || !row_stride_ok(ldy, cfg->D, bf ? 2 : 4) || !aligned16(h0) ||
+      !aligned16(h_last) || !aligned16(states) || !aligned16(ws) || (ws == nullptr && need > 0))
     return MATE_ERR_ARG;
-  if (ws_bytes < mate_gated_scan_workspace_bytes(cfg)) return MATE_ERR_WORKSPACE;
+  if (ws_bytes < need) return MATE_ERR_WORKSPACE;
+  const GatedScanScratch s = carve_gated(cfg, ws, false);
   p.h0 = h0;
   p.y = y;
-  p.ldy = ldy;
+  p.ldy = static_cast<unsigned>(ldy);
   p.h_last = h_last;
   p.states = states;
+  p.pair = s.pair;
+  p.carry = s.carry;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   t_launches = 0;
-  const bool bf = cfg->dtype == MATE_BF16;
-  if (p.n <= kGsShort) {
-    const long long threads = (long long)cfg->B * (cfg->D / 2);
-    const int blocks = static_cast<int>((threads + 127) / 128);
-    trace_begin(MATE_K_GATED_SCAN, st);
-    if (bf) gated_scan_short_kernel<__nv_bfloat16><<<blocks, 128, 0, st>>>(p);
-    else gated_scan_short_kernel<float><<<blocks, 128, 0, st>>>(p);
+  const int blocks = gated_blocks(&p, 2);
+  if (p.chunks > 1) {
+    trace_begin(MATE_K_GATED_SCAN_PAIRS, st);
+    if (bf) gated_scan_kernel<__nv_bfloat16, false><<<blocks, 256, 0, st>>>(p);
+    else gated_scan_kernel<float, false><<<blocks, 256, 0, st>>>(p);
     MATE_LAUNCH_CHECK();
-    return MATE_OK;
+    MATE_TRY(launch_carry(p, h0, 0, st));
   }
-  return launch_gated(bf ? gated_scan_kernel<__nv_bfloat16> : gated_scan_kernel<float>, MATE_K_GATED_SCAN,
-                      bf ? sizeof(GsSmem<__nv_bfloat16, 2>) : sizeof(GsSmem<float, 2>), p, bf,
-                      carve_gated(cfg, ws, false), ws, st);
+  trace_begin(MATE_K_GATED_SCAN, st);
+  if (bf) gated_scan_kernel<__nv_bfloat16, true><<<blocks, 256, 0, st>>>(p);
+  else gated_scan_kernel<float, true><<<blocks, 256, 0, st>>>(p);
+  MATE_LAUNCH_CHECK();
+  return MATE_OK;
 }
 
 size_t mate_gated_scan_backward_workspace_bytes(const mate_gated_scan_config* cfg) {
   if (check_gated(cfg) != MATE_OK) return 0;
-  return carve_gated(cfg, nullptr, true).total;
+  return carve_gated(cfg, nullptr, true).bytes;
 }
 
 mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g, long long ldg, const float* bias,
@@ -348,7 +358,8 @@ mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g
   MATE_TRY(check_gated(cfg));
   GatedScanParams p{};
   MATE_TRY(fill_gated(cfg, x, ldx, g, ldg, bias, &p));
-  const int es = cfg->dtype == MATE_BF16 ? 2 : 4;
+  const bool bf = cfg->dtype == MATE_BF16;
+  const int es = bf ? 2 : 4;
   if (states == nullptr || dy == nullptr || dx == nullptr || dg == nullptr || ws == nullptr || !aligned16(states) ||
       !aligned16(dy) || !aligned16(dx) || !aligned16(dg) || !aligned16(dh_last) || !aligned16(dbias) ||
       !aligned16(dh0) || !aligned16(ws) || !row_stride_ok(lddy, cfg->D, es) || !row_stride_ok(lddx, cfg->D, es) ||
@@ -358,25 +369,37 @@ mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g
     if (dx == in || dg == in) return MATE_ERR_ARG;
   if (dx == dg) return MATE_ERR_ARG;
   if (ws_bytes < mate_gated_scan_backward_workspace_bytes(cfg)) return MATE_ERR_WORKSPACE;
+  const GatedScanScratch s = carve_gated(cfg, ws, true);
   p.states = const_cast<float*>(states);
   p.dy = dy;
-  p.lddy = lddy;
+  p.lddy = static_cast<unsigned>(lddy);
   p.dh_last = dh_last;
   p.dx = dx;
-  p.lddx = lddx;
+  p.lddx = static_cast<unsigned>(lddx);
   p.dg = dg;
-  p.lddg = lddg;
-  const GatedScanScratch s = carve_gated(cfg, ws, true);
+  p.lddg = static_cast<unsigned>(lddg);
   p.dbias_part = dbias != nullptr ? s.dbias_part : nullptr;
   p.dh0 = dh0;
+  p.pair = s.pair;
+  p.carry = s.carry;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   t_launches = 0;
-  const bool bf = cfg->dtype == MATE_BF16;
-  MATE_TRY(launch_gated(bf ? gated_scan_bwd_kernel<__nv_bfloat16> : gated_scan_bwd_kernel<float>, MATE_K_GATED_SCAN_BWD,
-                        bf ? sizeof(GsSmem<__nv_bfloat16, 3>) : sizeof(GsSmem<float, 3>), p, bf, s, ws, st));
+  if (p.chunks > 1) {
+    const int blocks = gated_blocks(&p, 2);
+    trace_begin(MATE_K_GATED_SCAN_PAIRS, st);
+    if (bf) gated_adjoint_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(p);
+    else gated_adjoint_kernel<float><<<blocks, 256, 0, st>>>(p);
+    MATE_LAUNCH_CHECK();
+    MATE_TRY(launch_carry(p, dh_last, 1, st));
+  }
+  const int blocks = gated_blocks(&p, 1);
+  trace_begin(MATE_K_GATED_SCAN_BWD, st);
+  if (bf) gated_scan_bwd_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(p);
+  else gated_scan_bwd_kernel<float><<<blocks, 256, 0, st>>>(p);
+  MATE_LAUNCH_CHECK();
   if (dbias != nullptr) {
     trace_begin(MATE_K_GATED_SCAN_BIAS, st);
-    sum_parts_kernel<<<ceil_div(cfg->D, 32), 1024, 0, st>>>(s.dbias_part, cfg->B * p.tiles, cfg->D, dbias, cfg->D, nullptr);
+    sum_parts_kernel<<<ceil_div(cfg->D, 32), 1024, 0, st>>>(s.dbias_part, cfg->B * p.chunks, cfg->D, dbias, cfg->D, nullptr);
     MATE_LAUNCH_CHECK();
   }
   return MATE_OK;
