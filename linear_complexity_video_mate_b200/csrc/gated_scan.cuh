@@ -19,10 +19,14 @@
 #include "common.cuh"
 #include "mamba_extras.cuh"   // to_f32, from_f32
 
+#include <type_traits>
+
 namespace mate {
 
 constexpr int kGsState = 8;      // rows per saved state: the backward pass holds so many rows of a channel pair at a time
-constexpr int kGsBatch = 8;      // rows that a thread loads at a time
+constexpr int kGsBatch = kGsState;   // rows that a thread loads at a time
+constexpr int kGsThreads = 128;
+static_assert(kGsBatch == kGsState, "a state is saved before every batch of rows");
 constexpr int kGsMaxChunk = 128;
 constexpr int kGsOneChunk = 64;  // sequences up to this length are one chunk
 constexpr int kGsCarryCh = 16, kGsCarrySeg = 64;   // channels of a block of the carry kernel, runs of chunks it cuts them into
@@ -66,6 +70,22 @@ struct GsWalk {
     // every step s0, every wrap of the first counter d1 more, every wrap of the second d2 more (mod 2^32 on the way)
     row = static_cast<int>(static_cast<unsigned>(o.base) + s * static_cast<unsigned>(o.s0) +
                            q * static_cast<unsigned>(o.d1) + q2 * static_cast<unsigned>(o.d2));
+  }
+  // The next U rows; usually the first counter does not start again among them.
+  template <int U>
+  __device__ __forceinline__ void take(const GsOrder& o, int (&r)[U]) {
+    if (c0 + U < static_cast<int>(o.n0.d)) {
+#pragma unroll
+      for (int j = 0; j < U; ++j) r[j] = row + j * o.s0;
+      row += U * o.s0;
+      c0 += U;
+    } else {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        r[j] = row;
+        next(o);
+      }
+    }
   }
   __device__ __forceinline__ void next(const GsOrder& o) {
     row += o.s0;
@@ -163,7 +183,7 @@ struct GsItem {
 // Four channels of a chunk per thread.  OUT: y from the state before the chunk (and the states every kGsState rows, the
 // last state); else the chunk's pair.
 template <typename T_, bool OUT>
-__global__ void __launch_bounds__(256) gated_scan_kernel(const GatedScanParams p) {
+__global__ void __launch_bounds__(kGsThreads, !OUT && sizeof(T_) == 2 ? 8 : 1) gated_scan_kernel(const GatedScanParams p) {
   constexpr int NP = 2, U = kGsBatch;
   unsigned t = blockIdx.x * blockDim.x + threadIdx.x;
   if (OUT) t = gridDim.x * blockDim.x - 1 - t;   // from the end: the rows that the first step read last
@@ -190,26 +210,25 @@ __global__ void __launch_bounds__(256) gated_scan_kernel(const GatedScanParams p
   float* st = OUT && p.states != nullptr
                   ? p.states + ((long long)it.b * p.states_per + s0 / kGsState) * p.D + it.c : nullptr;
   GsWalk w(p.order, s0);
-  for (int i = 0; i < rows; i += U) {
+  auto batch = [&](int i, auto all) {   // all U rows are there, or up to the end
+    constexpr bool whole = decltype(all)::value;
     int row[U];
     GsRaw<T_, NP> xr[U], gr[U];
+    w.take(p.order, row);
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      row[j] = w.row;
-      w.next(p.order);
-      if (i + j < rows) {
+    for (int j = 0; j < U; ++j)
+      if (whole || i + j < rows) {
         xr[j].load(gs_at(x, row[j], p.ldx));
         gr[j].load(gs_at(g, row[j], p.ldg));
       }
-    }
-    if (OUT && st != nullptr && i % kGsState == 0) {
+    if (OUT && st != nullptr) {
 #pragma unroll
       for (int k = 0; k < NP; ++k) reinterpret_cast<float2*>(st)[k] = h[k];
       st += p.D;
     }
 #pragma unroll
     for (int j = 0; j < U; ++j)
-      if (i + j < rows) {
+      if (whole || i + j < rows) {
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
           float2 a, na;
@@ -219,7 +238,10 @@ __global__ void __launch_bounds__(256) gated_scan_kernel(const GatedScanParams p
         }
         if (OUT) gs_store<T_, NP>(gs_at(y, row[j], p.ldy), h);
       }
-  }
+  };
+  int i = 0;
+  for (; i + U <= rows; i += U) batch(i, std::true_type{});
+  if (i < rows) batch(i, std::false_type{});
   if (OUT) {
     if (p.h_last != nullptr && it.k + 1 == p.chunks)
 #pragma unroll
@@ -233,7 +255,7 @@ __global__ void __launch_bounds__(256) gated_scan_kernel(const GatedScanParams p
 
 // The chunks' pairs of the adjoint state, m -> A m + M from the row behind a chunk to the row before it.
 template <typename T_>
-__global__ void __launch_bounds__(256) gated_adjoint_kernel(const GatedScanParams p) {
+__global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 2 ? 8 : 1) gated_adjoint_kernel(const GatedScanParams p) {
   constexpr int NP = 2, U = kGsBatch;
   const unsigned t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= p.threads) return;
@@ -251,19 +273,20 @@ __global__ void __launch_bounds__(256) gated_adjoint_kernel(const GatedScanParam
   const T_* g = static_cast<const T_*>(p.g) + (long long)it.b * p.n * p.ldg + it.c;
   const T_* dy = static_cast<const T_*>(p.dy) + (long long)it.b * p.n * p.lddy + it.c;
   GsWalk w(p.back, p.n - s0 - rows);
-  for (int i = 0; i < rows; i += U) {
+  auto batch = [&](int i, auto all) {
+    constexpr bool whole = decltype(all)::value;
+    int row[U];
     GsRaw<T_, NP> gr[U], dr[U];
-#pragma unroll
-    for (int j = 0; j < U; ++j) {
-      if (i + j < rows) {
-        gr[j].load(gs_at(g, w.row, p.ldg));
-        dr[j].load(gs_at(dy, w.row, p.lddy));
-      }
-      w.next(p.back);
-    }
+    w.take(p.back, row);
 #pragma unroll
     for (int j = 0; j < U; ++j)
-      if (i + j < rows)
+      if (whole || i + j < rows) {
+        gr[j].load(gs_at(g, row[j], p.ldg));
+        dr[j].load(gs_at(dy, row[j], p.lddy));
+      }
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (whole || i + j < rows)
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
           float2 e;
@@ -271,7 +294,10 @@ __global__ void __launch_bounds__(256) gated_adjoint_kernel(const GatedScanParam
           m[k] = mul_f32x2(a, add2(dr[j].get(k), m[k]));
           A[k] = mul_f32x2(A[k], a);
         }
-  }
+  };
+  int i = 0;
+  for (; i + U <= rows; i += U) batch(i, std::true_type{});
+  if (i < rows) batch(i, std::false_type{});
   float4* o = reinterpret_cast<float4*>(p.pair + (long long)it.k * p.B.d * p.D + it.bc);
 #pragma unroll
   for (int k = 0; k < NP; ++k) o[k] = make_float4(A[k].x, m[k].x, A[k].y, m[k].y);
@@ -313,7 +339,7 @@ __global__ void __launch_bounds__(kGsCarryCh * kGsCarrySeg)
 // Gradients: two channels of a chunk per thread, kGsState rows at a time from the last to the first.  Their states are
 // formed again from the saved one, then the adjoint state walks back over them.
 template <typename T_>
-__global__ void __launch_bounds__(256) gated_scan_bwd_kernel(const GatedScanParams p) {
+__global__ void __launch_bounds__(kGsThreads) gated_scan_bwd_kernel(const GatedScanParams p) {
   constexpr int U = kGsState;
   const unsigned t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= p.threads) return;
@@ -332,15 +358,24 @@ __global__ void __launch_bounds__(256) gated_scan_bwd_kernel(const GatedScanPara
   T_* dg = static_cast<T_*>(p.dg) + (long long)it.b * p.n * p.lddg + it.c;
   const float* st = p.states + ((long long)it.b * p.states_per + s0 / kGsState) * p.D + it.c;
   GsWalk w(p.back, p.n - s0 - rows);
-  for (int i = (rows - 1) / U * U; i >= 0; i -= U) {
-    const int cnt = min(U, rows - i);   // below U for the last rows of the sequence only
-    int row[U];
+  auto batch = [&](int i, auto all) {   // rows i .. i + U - 1 of the chunk (or up to its end), last to first
+    constexpr bool whole = decltype(all)::value;
+    int row[U];   // from the last one back
     GsRaw<T_, 1> xr[U], gr[U], dr[U];
+    const int skip = whole ? 0 : U - (rows - i);   // rows behind the end
+    if (whole) {
+      w.take(p.back, row);
+    } else {
 #pragma unroll
-    for (int j = U - 1; j >= 0; --j)
-      if (j < cnt) {
-        row[j] = w.row;
-        w.next(p.back);
+      for (int j = 0; j < U; ++j)
+        if (j >= skip) {
+          row[j] = w.row;
+          w.next(p.back);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (whole || j >= skip) {
         xr[j].load(gs_at(x, row[j], p.ldx));
         gr[j].load(gs_at(g, row[j], p.ldg));
         dr[j].load(gs_at(dy, row[j], p.lddy));
@@ -348,16 +383,16 @@ __global__ void __launch_bounds__(256) gated_scan_bwd_kernel(const GatedScanPara
     float2 h = __ldg(reinterpret_cast<const float2*>(st + (long long)(i / U) * p.D));
     float2 a[U], na[U], d[U];   // d: the state before the row, less x
 #pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (j < cnt) {
+    for (int j = U - 1; j >= 0; --j)
+      if (whole || j >= skip) {
         const float2 xv = xr[j].get(0);
         gs_gate(fma2(gr[j].get(0), both(kGsLog2e), bias[0]), &a[j], &na[j]);
         d[j] = fma2(xv, both(-1.f), h);
         h = fma2(a[j], h, mul_f32x2(na[j], xv));
       }
 #pragma unroll
-    for (int j = U - 1; j >= 0; --j)
-      if (j < cnt) {
+    for (int j = 0; j < U; ++j)
+      if (whole || j >= skip) {
         const float2 l = add2(dr[j].get(0), m[0]);
         const float2 o[1] = {mul_f32x2(na[j], l)};
         m[0] = mul_f32x2(a[j], l);
@@ -366,7 +401,10 @@ __global__ void __launch_bounds__(256) gated_scan_bwd_kernel(const GatedScanPara
         gs_store<T_, 1>(gs_at(dg, row[j], p.lddg), v);
         db = add2(db, v[0]);
       }
-  }
+  };
+  int i = rows / U * U;
+  if (i < rows) batch(i, std::false_type{});
+  for (i -= U; i >= 0; i -= U) batch(i, std::true_type{});
   if (it.k == 0 && p.dh0 != nullptr) *reinterpret_cast<float2*>(p.dh0 + it.bc) = m[0];
   if (p.dbias_part != nullptr) *reinterpret_cast<float2*>(p.dbias_part + (long long)it.k * p.B.d * p.D + it.bc) = db;
 }

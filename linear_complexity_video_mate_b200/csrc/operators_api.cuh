@@ -282,7 +282,7 @@ GatedScanScratch carve_gated(const mate_gated_scan_config* c, void* ws, bool bac
 int gated_blocks(GatedScanParams* p, int np) {
   p->per = FastDiv(p->D / (2 * np));
   p->threads = static_cast<unsigned>(p->chunks) * p->B.d * p->per.d;
-  return static_cast<int>((p->threads + 255u) / 256u);
+  return static_cast<int>((p->threads + kGsThreads - 1u) / kGsThreads);
 }
 
 mate_status launch_carry(const GatedScanParams& p, const float* start, int back, cudaStream_t st) {
@@ -333,14 +333,14 @@ mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long lo
   const int blocks = gated_blocks(&p, 2);
   if (p.chunks > 1) {
     trace_begin(MATE_K_GATED_SCAN_PAIRS, st);
-    if (bf) gated_scan_kernel<__nv_bfloat16, false><<<blocks, 256, 0, st>>>(p);
-    else gated_scan_kernel<float, false><<<blocks, 256, 0, st>>>(p);
+    if (bf) gated_scan_kernel<__nv_bfloat16, false><<<blocks, kGsThreads, 0, st>>>(p);
+    else gated_scan_kernel<float, false><<<blocks, kGsThreads, 0, st>>>(p);
     MATE_LAUNCH_CHECK();
     MATE_TRY(launch_carry(p, h0, 0, st));
   }
   trace_begin(MATE_K_GATED_SCAN, st);
-  if (bf) gated_scan_kernel<__nv_bfloat16, true><<<blocks, 256, 0, st>>>(p);
-  else gated_scan_kernel<float, true><<<blocks, 256, 0, st>>>(p);
+  if (bf) gated_scan_kernel<__nv_bfloat16, true><<<blocks, kGsThreads, 0, st>>>(p);
+  else gated_scan_kernel<float, true><<<blocks, kGsThreads, 0, st>>>(p);
   MATE_LAUNCH_CHECK();
   return MATE_OK;
 }
@@ -387,15 +387,15 @@ mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g
   if (p.chunks > 1) {
     const int blocks = gated_blocks(&p, 2);
     trace_begin(MATE_K_GATED_SCAN_PAIRS, st);
-    if (bf) gated_adjoint_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(p);
-    else gated_adjoint_kernel<float><<<blocks, 256, 0, st>>>(p);
+    if (bf) gated_adjoint_kernel<__nv_bfloat16><<<blocks, kGsThreads, 0, st>>>(p);
+    else gated_adjoint_kernel<float><<<blocks, kGsThreads, 0, st>>>(p);
     MATE_LAUNCH_CHECK();
     MATE_TRY(launch_carry(p, dh_last, 1, st));
   }
   const int blocks = gated_blocks(&p, 1);
   trace_begin(MATE_K_GATED_SCAN_BWD, st);
-  if (bf) gated_scan_bwd_kernel<__nv_bfloat16><<<blocks, 256, 0, st>>>(p);
-  else gated_scan_bwd_kernel<float><<<blocks, 256, 0, st>>>(p);
+  if (bf) gated_scan_bwd_kernel<__nv_bfloat16><<<blocks, kGsThreads, 0, st>>>(p);
+  else gated_scan_bwd_kernel<float><<<blocks, kGsThreads, 0, st>>>(p);
   MATE_LAUNCH_CHECK();
   if (dbias != nullptr) {
     trace_begin(MATE_K_GATED_SCAN_BIAS, st);
