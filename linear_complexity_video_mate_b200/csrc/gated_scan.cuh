@@ -183,7 +183,7 @@ struct GsItem {
 // Four channels of a chunk per thread.  OUT: y from the state before the chunk (and the states every kGsState rows, the
 // last state); else the chunk's pair.
 template <typename T_, bool OUT>
-__global__ void __launch_bounds__(kGsThreads, !OUT && sizeof(T_) == 2 ? 8 : 1) gated_scan_kernel(const GatedScanParams p) {
+__global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : OUT ? 6 : 8) gated_scan_kernel(const GatedScanParams p) {
   constexpr int NP = 2, U = kGsBatch;
   unsigned t = blockIdx.x * blockDim.x + threadIdx.x;
   if (OUT) t = gridDim.x * blockDim.x - 1 - t;   // from the end: the rows that the first step read last
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kGsThreads, !OUT && sizeof(T_) == 2 ? 8 : 1) g
 
 // The chunks' pairs of the adjoint state, m -> A m + M from the row behind a chunk to the row before it.
 template <typename T_>
-__global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 2 ? 8 : 1) gated_adjoint_kernel(const GatedScanParams p) {
+__global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : 8) gated_adjoint_kernel(const GatedScanParams p) {
   constexpr int NP = 2, U = kGsBatch;
   const unsigned t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= p.threads) return;
