@@ -25,7 +25,7 @@ namespace mate {
 
 constexpr int kGsState = 8;      // rows per saved state: the backward pass holds so many rows of a channel pair at a time
 constexpr int kGsBatch = kGsState;   // rows that a thread loads at a time
-constexpr int kGsThreads = 128;
+constexpr int kGsThreads = 128, kGsBwdThreads = 256;   // 1 KB of a bf16 row per block either way
 static_assert(kGsBatch == kGsState, "a state is saved before every batch of rows");
 constexpr int kGsMaxChunk = 128;
 constexpr int kGsOneChunk = 64;  // sequences up to this length are one chunk
@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(kGsCarryCh * kGsCarrySeg)
 // Gradients: two channels of a chunk per thread, kGsState rows at a time from the last to the first.  Their states are
 // formed again from the saved one, then the adjoint state walks back over them.
 template <typename T_>
-__global__ void __launch_bounds__(kGsThreads) gated_scan_bwd_kernel(const GatedScanParams p) {
+__global__ void __launch_bounds__(kGsBwdThreads, 2) gated_scan_bwd_kernel(const GatedScanParams p) {
   constexpr int U = kGsState;
   const unsigned t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= p.threads) return;

@@ -279,10 +279,10 @@ GatedScanScratch carve_gated(const mate_gated_scan_config* c, void* ws, bool bac
 }
 
 // Grid of a kernel whose threads take 2 np channels of a chunk.
-int gated_blocks(GatedScanParams* p, int np) {
+int gated_blocks(GatedScanParams* p, int np, int threads) {
   p->per = FastDiv(p->D / (2 * np));
   p->threads = static_cast<unsigned>(p->chunks) * p->B.d * p->per.d;
-  return static_cast<int>((p->threads + kGsThreads - 1u) / kGsThreads);
+  return static_cast<int>((p->threads + threads - 1u) / threads);
 }
 
 mate_status launch_carry(const GatedScanParams& p, const float* start, int back, cudaStream_t st) {
@@ -330,7 +330,7 @@ mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long lo
   p.carry = s.carry;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   t_launches = 0;
-  const int blocks = gated_blocks(&p, 2);
+  const int blocks = gated_blocks(&p, 2, kGsThreads);
   if (p.chunks > 1) {
     trace_begin(MATE_K_GATED_SCAN_PAIRS, st);
     if (bf) gated_scan_kernel<__nv_bfloat16, false><<<blocks, kGsThreads, 0, st>>>(p);
@@ -385,17 +385,17 @@ mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   t_launches = 0;
   if (p.chunks > 1) {
-    const int blocks = gated_blocks(&p, 2);
+    const int blocks = gated_blocks(&p, 2, kGsThreads);
     trace_begin(MATE_K_GATED_SCAN_PAIRS, st);
     if (bf) gated_adjoint_kernel<__nv_bfloat16><<<blocks, kGsThreads, 0, st>>>(p);
     else gated_adjoint_kernel<float><<<blocks, kGsThreads, 0, st>>>(p);
     MATE_LAUNCH_CHECK();
     MATE_TRY(launch_carry(p, dh_last, 1, st));
   }
-  const int blocks = gated_blocks(&p, 1);
+  const int blocks = gated_blocks(&p, 1, kGsBwdThreads);
   trace_begin(MATE_K_GATED_SCAN_BWD, st);
-  if (bf) gated_scan_bwd_kernel<__nv_bfloat16><<<blocks, kGsThreads, 0, st>>>(p);
-  else gated_scan_bwd_kernel<float><<<blocks, kGsThreads, 0, st>>>(p);
+  if (bf) gated_scan_bwd_kernel<__nv_bfloat16><<<blocks, kGsBwdThreads, 0, st>>>(p);
+  else gated_scan_bwd_kernel<float><<<blocks, kGsBwdThreads, 0, st>>>(p);
   MATE_LAUNCH_CHECK();
   if (dbias != nullptr) {
     trace_begin(MATE_K_GATED_SCAN_BIAS, st);
