@@ -45,44 +45,66 @@ __device__ __forceinline__ int quant_round_tiny(float x, float s) {
   return static_cast<int>(fmin(fmax(rint(static_cast<double>(x) / static_cast<double>(s)), -127.0), 127.0));
 }
 
-constexpr int kQuantHeld = 8;   // 16-byte vectors of a row that a thread holds between its two passes
+// The larger magnitude (NaN if either is one; the sign means nothing), of two packed bf16 or of an fp32 value.
+template <typename T_>
+__device__ __forceinline__ uint32_t quant_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  if constexpr (sizeof(T_) == 2) asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else asm("{\n .reg .f32 x, y, z;\n mov.b32 x, %1;\n mov.b32 y, %2;\n max.NaN.xorsign.abs.f32 z, x, y;\n mov.b32 %0, z;\n}"
+           : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
-// G threads per row (a warp, or a block where there are few rows), 16-byte loads.  The first kQuantHeld vectors of a
-// thread stay in registers, so that a row of up to G * 128 bytes is read once; the rest is read again (from L2).  A row
-// with an infinity or NaN gets scale NaN and q = 0, so that the projection of that row is NaN.
-template <typename T_, int G>
-__global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const T_* __restrict__ x, long long ldx, long long M, int K,
+// A row's 16 bytes j, quantised and stored; whether a value next to a midpoint is among them.
+template <typename T_>
+__device__ __forceinline__ bool quant_put(int8_t* qr, int j, const uint4& u, float inv) {
+  float off = 0.f;
+  if constexpr (sizeof(T_) == 2) {
+    const float2 a = quant_near(bf16_pair(u.x), inv, &off), b = quant_near(bf16_pair(u.y), inv, &off);
+    const float2 c = quant_near(bf16_pair(u.z), inv, &off), d = quant_near(bf16_pair(u.w), inv, &off);
+    reinterpret_cast<uint2*>(qr)[j] = make_uint2(quant_bytes(a, b), quant_bytes(c, d));
+  } else {
+    const float2 a = quant_near(make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), inv, &off);
+    const float2 b = quant_near(make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), inv, &off);
+    reinterpret_cast<uint32_t*>(qr)[j] = quant_bytes(a, b);
+  }
+  return off > kQuantMid;
+}
+
+// G threads per row (a warp, or a block where there are few rows or long ones), 16-byte loads.  NV > 0: a thread holds
+// the row's NV vectors t, t + G, .. between the two passes, so that the row is read once; NV = 0: rows of any length, read
+// twice (the second time from L2).  A row with an infinity or NaN gets scale NaN and q = 0, so that the projection of that
+// row is NaN.
+template <typename T_, int G, int NV>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const T_* __restrict__ x, long long ldx, int M, int K,
                                                             int8_t* __restrict__ q, long long ldq,
                                                             float* __restrict__ scale) {
   constexpr int V = 16 / sizeof(T_);
-  __shared__ unsigned s_mx[8];
+  __shared__ uint32_t s_mx[8];
   const int t = threadIdx.x % G, lane = threadIdx.x & 31;
   const int nv = K / V;   // whole vectors; the rest of the row goes value by value
-  const long long per = blockDim.x / G;
-  for (long long r = blockIdx.x * per + threadIdx.x / G; r < M; r += gridDim.x * per) {
+  const int per = 256 / G, step = gridDim.x * per;
+  for (int r = blockIdx.x * per + threadIdx.x / G; r < M; r += step) {
     const T_* xr = x + r * ldx;
+    const uint4* xv = reinterpret_cast<const uint4*>(xr);
     int8_t* qr = q + r * ldq;
-    uint4 h[kQuantHeld];
-    unsigned mx = 0;   // |x| as bits: ordered like the values, NaN above infinity (bf16: two 16-bit halves, joined below)
-    auto take = [&](const uint4& u) {
-      if constexpr (sizeof(T_) == 2)
-        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
-                                   __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
-      else
-        mx = max(mx, max(max(u.x & 0x7fffffffu, u.y & 0x7fffffffu), max(u.z & 0x7fffffffu, u.w & 0x7fffffffu)));
-    };
+    uint4 h[NV > 0 ? NV : 1];
+    uint32_t mx = 0;   // magnitudes as bits (bf16: two at a time): ordered like the values, NaN above infinity
+    if constexpr (NV > 0) {
 #pragma unroll
-    for (int j = 0; j < kQuantHeld; ++j) {
-      if (j * G >= nv) break;   // the same for all
-      h[j] = t + j * G < nv ? __ldg(reinterpret_cast<const uint4*>(xr) + t + j * G) : make_uint4(0, 0, 0, 0);
-    }
+      for (int j = 0; j < NV; ++j) h[j] = t + j * G < nv ? __ldg(xv + t + j * G) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int j = 0; j < kQuantHeld; ++j) {
-      if (j * G >= nv) break;
-      take(h[j]);
+      for (int j = 0; j < NV; ++j)
+        mx = quant_max<T_>(mx, quant_max<T_>(quant_max<T_>(h[j].x, h[j].y), quant_max<T_>(h[j].z, h[j].w)));
+    } else {
+#pragma unroll 4
+      for (int j = t; j < nv; j += G) {
+        const uint4 u = __ldg(xv + j);
+        mx = quant_max<T_>(mx, quant_max<T_>(quant_max<T_>(u.x, u.y), quant_max<T_>(u.z, u.w)));
+      }
     }
-    for (int j = t + kQuantHeld * G; j < nv; j += G) take(__ldg(reinterpret_cast<const uint4*>(xr) + j));
-    if constexpr (sizeof(T_) == 2) mx = max(mx << 16, mx & 0xffff0000u);
+    if constexpr (sizeof(T_) == 2) mx = max((mx << 16) & 0x7fffffffu, mx & 0x7fff0000u);
+    else mx &= 0x7fffffffu;
     for (int c = nv * V + t; c < K; c += G) mx = max(mx, __float_as_uint(to_f32(xr[c])) & 0x7fffffffu);
     mx = __reduce_max_sync(0xffffffffu, mx);
     if constexpr (G > 32) {
@@ -96,37 +118,27 @@ __global__ void __launch_bounds__(256, 4) quantize_rows_kernel(const T_* __restr
     const float s = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(mx) / 127.f;
     if (t == 0) scale[r] = s;
     if (bad || s < kQuantTiny) {   // rare
+#pragma unroll 1
       for (int c = t; c < K; c += G) qr[c] = static_cast<int8_t>(bad ? 0 : quant_round_tiny(to_f32(xr[c]), s));
       continue;
     }
     const float inv = 1.f / s;
-    auto put = [&](int j, const uint4& u) {   // whether a value next to a midpoint is among them
-      float off = 0.f;
-      if constexpr (sizeof(T_) == 2) {
-        const float2 a = quant_near(bf16_pair(u.x), inv, &off), b = quant_near(bf16_pair(u.y), inv, &off);
-        const float2 c = quant_near(bf16_pair(u.z), inv, &off), d = quant_near(bf16_pair(u.w), inv, &off);
-        reinterpret_cast<uint2*>(qr)[j] = make_uint2(quant_bytes(a, b), quant_bytes(c, d));
-      } else {
-        const float2 a = quant_near(make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), inv, &off);
-        const float2 b = quant_near(make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), inv, &off);
-        reinterpret_cast<uint32_t*>(qr)[j] = quant_bytes(a, b);
-      }
-      return off > kQuantMid;
-    };
-    // the few vectors with such a value (one value in about 16,000) are done again, one by one
+    // the few vectors with a value next to a midpoint (one value in about 16,000) are done again, one by one
     auto again = [&](int j) {
 #pragma unroll 1
       for (int e = 0; e < V; ++e) qr[j * V + e] = static_cast<int8_t>(quant_round(to_f32(xr[j * V + e]), s, inv));
     };
-    unsigned redo = 0;
+    if constexpr (NV > 0) {
+      unsigned redo = 0;
 #pragma unroll
-    for (int j = 0; j < kQuantHeld; ++j) {
-      if (j * G >= nv) break;
-      if (t + j * G < nv && put(t + j * G, h[j])) redo |= 1u << j;
+      for (int j = 0; j < NV; ++j)
+        if (t + j * G < nv && quant_put<T_>(qr, t + j * G, h[j], inv)) redo |= 1u << j;
+#pragma unroll 1
+      for (; redo != 0; redo &= redo - 1) again(t + (__ffs(redo) - 1) * G);
+    } else {
+      for (int j = t; j < nv; j += G)
+        if (quant_put<T_>(qr, j, __ldg(xv + j), inv)) again(j);
     }
-    for (int j = t + kQuantHeld * G; j < nv; j += G)
-      if (put(j, __ldg(reinterpret_cast<const uint4*>(xr) + j))) again(j);
-    for (; redo != 0; redo &= redo - 1) again(t + (__ffs(redo) - 1) * G);
     for (int c = nv * V + t; c < K; c += G) qr[c] = static_cast<int8_t>(quant_round(to_f32(xr[c]), s, inv));
   }
 }

@@ -437,18 +437,23 @@ bool make_tmap_out(CUtensorMap* m, void* ptr, long long rows, int cols, long lon
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A warp per row where there are enough rows to fill the SMs, else a block per row.
+// A warp per row where there are rows enough to fill the SMs and a warp can hold one, else a block per row.
+template <typename T_, int G>
+auto quantize_kernel_of(int vectors) -> void (*)(const T_*, long long, int, int, int8_t*, long long, float*) {
+  if (vectors <= G) return quantize_rows_kernel<T_, G, 1>;
+  if (vectors <= 2 * G) return quantize_rows_kernel<T_, G, 2>;
+  if (vectors <= 4 * G) return quantize_rows_kernel<T_, G, 4>;
+  if (G > 32 && vectors > 8 * G) return quantize_rows_kernel<T_, 256, 0>;
+  return quantize_rows_kernel<T_, G, 8>;
+}
+
 template <typename T_>
-void launch_quantize(const T_* x, long long ldx, long long M, int K, void* q, long long ldq, float* scale,
-                     cudaStream_t st) {
-  int8_t* q8 = static_cast<int8_t*>(q);
-  const long long sms = device_sms();
-  if (M >= 16 * sms)
-    quantize_rows_kernel<T_, 32>
-        <<<static_cast<int>(std::min<long long>((M + 7) / 8, 8 * sms)), 256, 0, st>>>(x, ldx, M, K, q8, ldq, scale);
-  else
-    quantize_rows_kernel<T_, 256>
-        <<<static_cast<int>(std::min<long long>(M, 8 * sms)), 256, 0, st>>>(x, ldx, M, K, q8, ldq, scale);
+void launch_quantize(const T_* x, long long ldx, int M, int K, void* q, long long ldq, float* scale, cudaStream_t st) {
+  const int sms = device_sms(), vectors = K / (16 / static_cast<int>(sizeof(T_)));
+  const bool warps = M >= 16 * sms && vectors <= 8 * 32;
+  auto kernel = warps ? quantize_kernel_of<T_, 32>(vectors) : quantize_kernel_of<T_, 256>(vectors);
+  const int blocks = std::min(warps ? ceil_div(M, 8) : M, 8 * sms);
+  kernel<<<blocks, 256, 0, st>>>(x, ldx, M, K, static_cast<int8_t*>(q), ldq, scale);
 }
 
 template <typename T_>
@@ -478,8 +483,8 @@ mate_status mate_quantize_rows(const void* x, long long ldx, long long M, int K,
   if (M == 0) return MATE_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   trace_begin(MATE_K_QUANTIZE_ROWS, st);
-  if (dtype == MATE_BF16) launch_quantize(static_cast<const __nv_bfloat16*>(x), ldx, M, K, q, ldq, scale, st);
-  else launch_quantize(static_cast<const float*>(x), ldx, M, K, q, ldq, scale, st);
+  if (dtype == MATE_BF16) launch_quantize(static_cast<const __nv_bfloat16*>(x), ldx, static_cast<int>(M), K, q, ldq, scale, st);
+  else launch_quantize(static_cast<const float*>(x), ldx, static_cast<int>(M), K, q, ldq, scale, st);
   MATE_LAUNCH_CHECK();
   return MATE_OK;
 }
