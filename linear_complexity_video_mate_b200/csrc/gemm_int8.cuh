@@ -12,30 +12,37 @@ namespace mate {
 // Rows to int8: scale = max|x| / 127 (fp32), q = x / scale to the nearest integer, ties to even.
 // ---------------------------------------------------------------------------------------------------
 
-// x / s to the nearest integer k for two |x| <= 127.5 s: t = x (1/s) is off by at most 127 * 2^-23 < 2^-15, so rounding t
-// (by adding 1.5 * 2^23, which leaves k in the sum's low byte) is right unless t is within 2^-15 of a midpoint.  off: the
-// largest distance from the integer taken so far.
-__device__ __forceinline__ float2 quant_near(float2 x, float inv, float* off) {
-  const float2 t = mul_f32x2(x, both(inv));
-  const float2 m = add2(t, both(12582912.f));
-  const float2 d = fma2(add2(m, both(-12582912.f)), both(-1.f), t);
-  *off = fmaxf(*off, fmaxf(fabsf(d.x), fabsf(d.y)));
+// x / s to the nearest integer k, ties to even, for two |x| <= 127.5 s, exactly.  t = x (1/s) is off by at most
+// 127 * 2^-23, so k from t (by adding 1.5 * 2^23, which leaves k in the sum's low byte) is right or the neighbour of the
+// right one; the remainder x - k s, which one fma gives without error (it has at most as many bits as x where k is in
+// doubt), tells: beyond s / 2, k is one off.  Where the remainder is just s / 2, t decides alone: TIES looks at those, too.
+// bf16 rows need that only if s has few bits (quant_ties), and quotients near midpoints are common there (x and the row's
+// maximum are ratios of small integers), so the correction has no branch.
+template <bool TIES>
+__device__ __forceinline__ float2 quant_two(float2 x, float inv, float s, float hs) {
+  float2 m = add2(mul_f32x2(x, both(inv)), both(12582912.f));
+  const float2 e = fma2(add2(m, both(-12582912.f)), both(-s), x);
+  bool px = fabsf(e.x) > hs, py = fabsf(e.y) > hs;
+  if (TIES) {
+    px = px || (fabsf(e.x) == hs && (__float_as_uint(m.x) & 1u));
+    py = py || (fabsf(e.y) == hs && (__float_as_uint(m.y) & 1u));
+  }
+  if (px) m.x += copysignf(1.f, e.x);
+  if (py) m.y += copysignf(1.f, e.y);
   return m;
 }
 __device__ __forceinline__ uint32_t quant_bytes(float2 lo, float2 hi) {
   return __byte_perm(__byte_perm(__float_as_uint(lo.x), __float_as_uint(lo.y), 0x0040),
                      __byte_perm(__float_as_uint(hi.x), __float_as_uint(hi.y), 0x0040), 0x5410);
 }
-constexpr float kQuantMid = 0.5f - 1.f / 32768;
-
-// The same, decided exactly: the remainder x - k s, which one fma gives without error next to a midpoint (it has at most
-// as many bits as x there), ties to even.
-__device__ __forceinline__ uint32_t quant_round(float x, float s, float inv) {
-  float k = rintf(x * inv);
-  const float e2 = 2.f * fmaf(-k, s, x);
-  if (e2 > s || (e2 == s && (static_cast<int>(k) & 1))) k += 1.f;
-  else if (e2 < -s || (e2 == -s && (static_cast<int>(k) & 1))) k -= 1.f;
-  return static_cast<uint32_t>(static_cast<int>(k));
+__device__ __forceinline__ int8_t quant_one(float x, float inv, float s, float hs) {
+  return static_cast<int8_t>(__float_as_uint(quant_two<true>(make_float2(x, 0.f), inv, s, hs).x));
+}
+// Whether a bf16 x can be (k + 1/2) s with t inexact: s has at most 8 significant bits and is no power of two (whose
+// reciprocal, and with it t, is exact).
+__device__ __forceinline__ bool quant_ties(float s) {
+  const uint32_t m = __float_as_uint(s) & 0x7fffffu;
+  return (m & 0xffffu) == 0 && m != 0;
 }
 
 constexpr float kQuantTiny = 1e-30f;   // scales below: 1 / s may overflow, the quotient is formed in 64 bits
@@ -55,20 +62,18 @@ __device__ __forceinline__ uint32_t quant_max(uint32_t a, uint32_t b) {
   return r;
 }
 
-// A row's 16 bytes j, quantised and stored; whether a value next to a midpoint is among them.
+// A row's 16 bytes j, quantised and stored.
 template <typename T_>
-__device__ __forceinline__ bool quant_put(int8_t* qr, int j, const uint4& u, float inv) {
-  float off = 0.f;
+__device__ __forceinline__ void quant_put(int8_t* qr, int j, const uint4& u, float inv, float s, float hs) {
   if constexpr (sizeof(T_) == 2) {
-    const float2 a = quant_near(bf16_pair(u.x), inv, &off), b = quant_near(bf16_pair(u.y), inv, &off);
-    const float2 c = quant_near(bf16_pair(u.z), inv, &off), d = quant_near(bf16_pair(u.w), inv, &off);
+    const float2 a = quant_two<false>(bf16_pair(u.x), inv, s, hs), b = quant_two<false>(bf16_pair(u.y), inv, s, hs);
+    const float2 c = quant_two<false>(bf16_pair(u.z), inv, s, hs), d = quant_two<false>(bf16_pair(u.w), inv, s, hs);
     reinterpret_cast<uint2*>(qr)[j] = make_uint2(quant_bytes(a, b), quant_bytes(c, d));
   } else {
-    const float2 a = quant_near(make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), inv, &off);
-    const float2 b = quant_near(make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), inv, &off);
+    const float2 a = quant_two<true>(make_float2(__uint_as_float(u.x), __uint_as_float(u.y)), inv, s, hs);
+    const float2 b = quant_two<true>(make_float2(__uint_as_float(u.z), __uint_as_float(u.w)), inv, s, hs);
     reinterpret_cast<uint32_t*>(qr)[j] = quant_bytes(a, b);
   }
-  return off > kQuantMid;
 }
 
 // G threads per row (a warp, or a block where there are few rows or long ones), 16-byte loads.  NV > 0: a thread holds
@@ -117,29 +122,23 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T_* __restrict
     const bool bad = mx >= 0x7f800000u;
     const float s = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(mx) / 127.f;
     if (t == 0) scale[r] = s;
-    if (bad || s < kQuantTiny) {   // rare
+    const float inv = 1.f / s, hs = 0.5f * s;
+    if (bad || s < kQuantTiny || (sizeof(T_) == 2 && quant_ties(s))) {   // rare
 #pragma unroll 1
-      for (int c = t; c < K; c += G) qr[c] = static_cast<int8_t>(bad ? 0 : quant_round_tiny(to_f32(xr[c]), s));
+      for (int c = t; c < K; c += G) {
+        const float v = to_f32(xr[c]);
+        qr[c] = bad ? 0 : s < kQuantTiny ? static_cast<int8_t>(quant_round_tiny(v, s)) : quant_one(v, inv, s, hs);
+      }
       continue;
     }
-    const float inv = 1.f / s;
-    // the few vectors with a value next to a midpoint (one value in about 16,000) are done again, one by one
-    auto again = [&](int j) {
-#pragma unroll 1
-      for (int e = 0; e < V; ++e) qr[j * V + e] = static_cast<int8_t>(quant_round(to_f32(xr[j * V + e]), s, inv));
-    };
     if constexpr (NV > 0) {
-      unsigned redo = 0;
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (t + j * G < nv && quant_put<T_>(qr, t + j * G, h[j], inv)) redo |= 1u << j;
-#pragma unroll 1
-      for (; redo != 0; redo &= redo - 1) again(t + (__ffs(redo) - 1) * G);
+        if (t + j * G < nv) quant_put<T_>(qr, t + j * G, h[j], inv, s, hs);
     } else {
-      for (int j = t; j < nv; j += G)
-        if (quant_put<T_>(qr, j, __ldg(xv + j), inv)) again(j);
+      for (int j = t; j < nv; j += G) quant_put<T_>(qr, j, __ldg(xv + j), inv, s, hs);
     }
-    for (int c = nv * V + t; c < K; c += G) qr[c] = static_cast<int8_t>(quant_round(to_f32(xr[c]), s, inv));
+    for (int c = nv * V + t; c < K; c += G) qr[c] = quant_one(to_f32(xr[c]), inv, s, hs);
   }
 }
 
