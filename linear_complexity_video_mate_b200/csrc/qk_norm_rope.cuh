@@ -79,7 +79,6 @@ template <typename T_, int MODE, int NV>
 struct QkLane {
   static constexpr int V = 16 / sizeof(T_), P = V / 2, HV = V / 2;
   static constexpr int C = MODE == kQkAny ? V : P;   // (cos, sin) entries per unit
-  float2 w[2][NV][P];      // weights of q and k heads
   float2 cs[NV][C];        // the row's cos and sin (kQkHalves: first all cos, then all sin of the unit's pairs)
   int c[NV][2];            // first channel of the unit (kQkHalves: of its two halves)
   int axis[NV][C], idx[NV][C], partner[MODE == kQkAny ? NV : 1][MODE == kQkAny ? V : 1];
@@ -130,17 +129,11 @@ struct QkLane {
         idx[n][k] = i;
         if constexpr (MODE == kQkAny) partner[n][k] = s ? ~o : o;   // the second of a pair, negated
       }
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const int ch = c[n][2 * k / HV] + 2 * k % HV;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float* wt = q == 0 ? p.wq : p.wk;
-          w[q][n][k] = wt != nullptr ? make_float2(__ldg(wt + ch), __ldg(wt + ch + 1)) : both(1.f);
-        }
-      }
     }
   }
+
+  // First channel of pair k of unit n.
+  __device__ __forceinline__ int channel(int n, int k) const { return c[n][2 * k / HV] + 2 * k % HV; }
 
   // The row's cos and sin of this lane's channels.
   __device__ __forceinline__ void row(const QkParams& p, unsigned row) {
@@ -294,6 +287,16 @@ __global__ void __launch_bounds__(kQkWarps * 32, 2) qk_norm_rope_kernel(const Qk
   const float inv_tp = 1.f / p.tp;
   L l;
   l.init(p, lane % G, G);
+  float2 wt[2][NV][L::P];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+      for (int k = 0; k < L::P; ++k) {
+        const float* w = q == 0 ? p.wq : p.wk;
+        wt[q][n][k] = w != nullptr ? __ldg(reinterpret_cast<const float2*>(w + l.channel(n, k))) : both(1.f);
+      }
   for (unsigned u = blockIdx.x * kQkWarps + warp; u < units; u += gridDim.x * kQkWarps) {
     const QkUnit un(p, u);
     l.row(p, un.row);
@@ -326,7 +329,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, 2) qk_norm_rope_kernel(const Qk
 #pragma unroll
           for (int n = 0; n < NV; ++n)
 #pragma unroll
-            for (int k = 0; k < L::P; ++k) v[n][k] = mul_f32x2(mul_f32x2(v[n][k], both(r)), l.w[kind][n][k]);
+            for (int k = 0; k < L::P; ++k) v[n][k] = mul_f32x2(mul_f32x2(v[n][k], both(r)), wt[kind][n][k]);
           l.template rotate<false>(v, buf);
           if (head < h1)
 #pragma unroll
@@ -339,17 +342,31 @@ __global__ void __launch_bounds__(kQkWarps * 32, 2) qk_norm_rope_kernel(const Qk
   }
 }
 
+// The head that a slot of the warp takes in a turn (-1: none).
+__device__ __forceinline__ int qk_head(const QkParams& p, int turn, int turns_q, int hpw, int slot) {
+  const int q = turn * hpw + slot, k = (turn - turns_q) * hpw + slot;
+  return turn < turns_q ? (q < p.hq ? q : -1) : (k < p.hk ? p.hq + k : -1);
+}
+
 template <typename T_, int MODE, int NV, int G>
-__global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_bwd_kernel(const QkParams p) {
+__global__ void __launch_bounds__(kQkWarps * 32, 2) qk_norm_rope_bwd_kernel(const QkParams p) {
   using L = QkLane<T_, MODE, NV>;
-  constexpr int HPW = 32 / G, UN = NV == 1 ? 2 : 1;
+  constexpr int HPW = 32 / G, UN = NV == 1 ? 4 : 1;
   __shared__ float s_buf[MODE == kQkAny ? kQkWarps * 32 * NV * L::V : 1];
   __shared__ float s_dw[kQkWarps][2][kQkMaxDim];
+  __shared__ float s_w[2][kQkMaxDim];   // the weights: not in registers, which the loads ahead and the sums need
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, slot = lane / G;
   float* buf = s_buf + (MODE == kQkAny ? (warp * HPW + slot) * (G * NV * L::V) : 0);
   const unsigned units = static_cast<unsigned>(p.rows) * p.splits.d;   // below 2^31: rows are shared only where they are few
   const int splits = p.splits.d;
   const float inv_tp = 1.f / p.tp;
+  const int turns_q = (p.hq + HPW - 1) / HPW, turns = turns_q + (p.hk + HPW - 1) / HPW;
+  for (int i = threadIdx.x; i < 2 * p.tp; i += blockDim.x) {
+    const int q = i / p.tp, c = i - q * p.tp;
+    const float* w = q == 0 ? p.wq : p.wk;
+    s_w[q][c] = w != nullptr ? __ldg(w + c) : 1.f;
+  }
+  __syncthreads();
   L l;
   l.init(p, lane % G, G);
   float2 dw[2][NV][L::P];
@@ -365,54 +382,52 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_bwd_kernel(const Q
     const T_* x = static_cast<const T_*>(p.x) + un.row * p.ldx;
     const T_* dz = static_cast<const T_*>(p.dz) + un.row * p.ldz;
     T_* out = static_cast<T_*>(p.out) + un.row * p.ldo;
+    // turns of the warp: the q heads HPW at a time, then the k heads
+    for (int b = un.part; b < turns; b += UN * splits) {
+      uint4 raw[UN][NV], rawz[UN][NV];
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      const int h0 = kind == 0 ? 0 : p.hq, h1 = kind == 0 ? p.hq : p.hq + p.hk;
-      for (int b = h0 + un.part * HPW + slot; b - slot < h1; b += UN * splits * HPW) {
-        uint4 raw[UN][NV], rawz[UN][NV];
+      for (int j = 0; j < UN; ++j) {
+        const int head = qk_head(p, b + j * splits, turns_q, HPW, slot);
 #pragma unroll
-        for (int j = 0; j < UN; ++j) {
-          const int head = b + j * splits * HPW;
-#pragma unroll
-          for (int n = 0; n < NV; ++n) {
-            const bool ok = head < h1 && l.on[n];
-            raw[j][n] = ok ? l.load(x + head * p.tp, n) : make_uint4(0, 0, 0, 0);
-            rawz[j][n] = ok ? l.load(dz + head * p.tp, n) : make_uint4(0, 0, 0, 0);
-          }
+        for (int n = 0; n < NV; ++n) {
+          const bool ok = b + j * splits < turns && head >= 0 && l.on[n];
+          raw[j][n] = ok ? l.load(x + head * p.tp, n) : make_uint4(0, 0, 0, 0);
+          rawz[j][n] = ok ? l.load(dz + head * p.tp, n) : make_uint4(0, 0, 0, 0);
         }
+      }
 #pragma unroll
-        for (int j = 0; j < UN; ++j) {
-          const int head = b + j * splits * HPW;
-          if (head - slot >= h1) break;
-          float2 v[NV][L::P], g[NV][L::P], ss = both(0.f), gx = both(0.f);
+      for (int j = 0; j < UN; ++j) {
+        if (b + j * splits >= turns) break;
+        const int head = qk_head(p, b + j * splits, turns_q, HPW, slot), kind = b + j * splits >= turns_q;
+        float2 v[NV][L::P], g[NV][L::P], ss = both(0.f), gx = both(0.f);
 #pragma unroll
-          for (int n = 0; n < NV; ++n) {
-            L::unpack(raw[j][n], v[n]);
-            L::unpack(rawz[j][n], g[n]);
+        for (int n = 0; n < NV; ++n) {
+          L::unpack(raw[j][n], v[n]);
+          L::unpack(rawz[j][n], g[n]);
 #pragma unroll
-            for (int k = 0; k < L::P; ++k) ss = fma2(v[n][k], v[n][k], ss);
+          for (int k = 0; k < L::P; ++k) ss = fma2(v[n][k], v[n][k], ss);
+        }
+        const float r = rsqrtf(fmaf(group_sum(ss.x + ss.y, G), inv_tp, p.eps));
+        l.template rotate<true>(g, buf);
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int k = 0; k < L::P; ++k) {
+            v[n][k] = mul_f32x2(v[n][k], both(r));
+            if (kind == 0) dw[0][n][k] = fma2(g[n][k], v[n][k], dw[0][n][k]);
+            else dw[1][n][k] = fma2(g[n][k], v[n][k], dw[1][n][k]);
+            g[n][k] = mul_f32x2(g[n][k], *reinterpret_cast<const float2*>(&s_w[kind][l.channel(n, k)]));
+            gx = fma2(g[n][k], v[n][k], gx);
           }
-          const float r = rsqrtf(fmaf(group_sum(ss.x + ss.y, G), inv_tp, p.eps));
-          l.template rotate<true>(g, buf);
+        const float m = -group_sum(gx.x + gx.y, G) * inv_tp;
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+          for (int k = 0; k < L::P; ++k) g[n][k] = mul_f32x2(fma2(v[n][k], both(m), g[n][k]), both(r));
+        if (head >= 0)
 #pragma unroll
           for (int n = 0; n < NV; ++n)
-#pragma unroll
-            for (int k = 0; k < L::P; ++k) {
-              v[n][k] = mul_f32x2(v[n][k], both(r));
-              dw[kind][n][k] = fma2(g[n][k], v[n][k], dw[kind][n][k]);
-              g[n][k] = mul_f32x2(g[n][k], l.w[kind][n][k]);
-              gx = fma2(g[n][k], v[n][k], gx);
-            }
-          const float m = -group_sum(gx.x + gx.y, G) * inv_tp;
-#pragma unroll
-          for (int n = 0; n < NV; ++n)
-#pragma unroll
-            for (int k = 0; k < L::P; ++k) g[n][k] = mul_f32x2(fma2(v[n][k], both(m), g[n][k]), both(r));
-          if (head < h1)
-#pragma unroll
-            for (int n = 0; n < NV; ++n)
-              if (l.on[n]) l.store(out + head * p.tp, n, g[n]);
-        }
+            if (l.on[n]) l.store(out + head * p.tp, n, g[n]);
       }
     }
     if (p.copy_v) qk_copy_v(p, dz, out, un.part);
@@ -430,7 +445,7 @@ __global__ void __launch_bounds__(kQkWarps * 32) qk_norm_rope_bwd_kernel(const Q
           d.y += __shfl_xor_sync(0xffffffffu, d.y, o);
         }
         if (slot == 0 && l.on[n])
-          *reinterpret_cast<float2*>(&s_dw[warp][q][l.c[n][2 * k / L::HV] + 2 * k % L::HV]) = d;
+          *reinterpret_cast<float2*>(&s_dw[warp][q][l.channel(n, k)]) = d;
       }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * p.tp; i += blockDim.x) {
