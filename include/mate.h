@@ -454,7 +454,7 @@ MATE_API mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, 
  *   x, g, y   rows b*T*H*W + (t*H + h)*W + w of D channels, row strides ldx, ldg, ldy in elements (at least D and a
  *             multiple of 16 bytes); y must not overlap x or g
  *   bias [D] (null: 0), h0 [B, D] state before the first row (null: 0), h_last [B, D] state after the last row
- *             (null: not wanted), all float
+ *             (null: not wanted; may be h0), all float
  *   states    (null: not wanted) for the backward pass: mate_gated_scan_states_bytes(cfg) bytes, overwritten with
  *             the state before each run of rows
  * Requirements: D a multiple of 16 bytes of elements, B*T*H*W < 2^31.  ws: at least
@@ -479,8 +479,8 @@ MATE_API mate_status mate_gated_scan(const void* x, long long ldx, const void* g
  * Backward pass of mate_gated_scan from its inputs, the `states` it wrote (same cfg; they hold h0), the gradient dy
  * of y and the gradient dh_last [B, D] of h_last (null: 0):
  *     l_t = dy_t + a_{t+1} l_{t+1},   dx_t = (1 - a_t) l_t,   dg_t = l_t (h_{t-1} - x_t) a_t (1 - a_t)
- * dbias [D] = sum of dg over samples and rows (null: not wanted), dh0 [B, D] = a_1 l_1 (null: not wanted), both
- * float, reproducible.  dx and dg must not overlap each other or an input.  ws: at least
+ * dbias [D] = sum of dg over samples and rows (null: not wanted), dh0 [B, D] = a_1 l_1 (null: not wanted; may
+ * be dh_last), both float, reproducible.  dx and dg must not overlap each other or an input.  ws: at least
  * mate_gated_scan_backward_workspace_bytes(cfg) bytes.
  */
 MATE_API size_t mate_gated_scan_backward_workspace_bytes(const mate_gated_scan_config* cfg);

@@ -157,7 +157,7 @@ template <int NP>
 __device__ __forceinline__ void gs_load_f32(const float* p, float2 (&v)[NP]) {
 #pragma unroll
   for (int k = 0; k < NP; ++k)
-    v[k] = p != nullptr ? __ldg(reinterpret_cast<const float2*>(p) + k) : make_float2(0.f, 0.f);
+    v[k] = p != nullptr ? reinterpret_cast<const float2*>(p)[k] : make_float2(0.f, 0.f);   // may be written later
 }
 
 // Row `row` behind p.
@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : OUT ? 6 : 8)
     h[k] = zero;
   }
   if (OUT) {
-    if (it.k > 0) gs_load_f32<NP>(p.carry + (long long)it.k * p.B.d * p.D + it.bc, h);
+    // several chunks: the first one's state comes from the carries too, since h_last may be h0
+    if (p.chunks > 1) gs_load_f32<NP>(p.carry + (long long)it.k * p.B.d * p.D + it.bc, h);
     else gs_load_f32<NP>(p.h0 != nullptr ? p.h0 + it.bc : nullptr, h);
   }
   const T_* x = static_cast<const T_*>(p.x) + (long long)it.b * p.n * p.ldx + it.c;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kGsBwdThreads, 2) gated_scan_bwd_kernel(const 
   float2 bias[1], m[1], db = both(0.f);
   gs_load_f32<1>(p.bias != nullptr ? p.bias + it.c : nullptr, bias);
   bias[0] = mul_f32x2(bias[0], both(kGsLog2e));
-  if (it.k + 1 < p.chunks) gs_load_f32<1>(p.carry + (long long)it.k * p.B.d * p.D + it.bc, m);
+  if (p.chunks > 1) gs_load_f32<1>(p.carry + (long long)it.k * p.B.d * p.D + it.bc, m);   // dh0 may be dh_last
   else gs_load_f32<1>(p.dh_last != nullptr ? p.dh_last + it.bc : nullptr, m);
   const T_* x = static_cast<const T_*>(p.x) + (long long)it.b * p.n * p.ldx + it.c;
   const T_* g = static_cast<const T_*>(p.g) + (long long)it.b * p.n * p.ldg + it.c;

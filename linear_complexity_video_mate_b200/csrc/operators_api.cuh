@@ -437,7 +437,8 @@ bool make_tmap_out(CUtensorMap* m, void* ptr, long long rows, int cols, long lon
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A warp per row where there are rows enough to fill the SMs and a warp can hold one, else a block per row.
+// A warp per row where there are rows enough to fill the SMs and a warp can hold one, else a block per row (bf16,
+// K = 2048: 512 rows 2.6 us by warps, 2.2 by blocks; 1184 rows 2.9 and 3.4; 4736 rows 5.4 and 8.8).
 template <typename T_, int G>
 auto quantize_kernel_of(int vectors) -> void (*)(const T_*, long long, int, int, int8_t*, long long, float*) {
   if (vectors <= G) return quantize_rows_kernel<T_, G, 1>;
@@ -450,7 +451,7 @@ auto quantize_kernel_of(int vectors) -> void (*)(const T_*, long long, int, int,
 template <typename T_>
 void launch_quantize(const T_* x, long long ldx, int M, int K, void* q, long long ldq, float* scale, cudaStream_t st) {
   const int sms = device_sms(), vectors = K / (16 / static_cast<int>(sizeof(T_)));
-  const bool warps = M >= 16 * sms && vectors <= 8 * 32;
+  const bool warps = M >= 6 * sms && vectors <= 8 * 32;
   auto kernel = warps ? quantize_kernel_of<T_, 32>(vectors) : quantize_kernel_of<T_, 256>(vectors);
   const int blocks = std::min(warps ? ceil_div(M, 8) : M, 8 * sms);
   kernel<<<blocks, 256, 0, st>>>(x, ldx, M, K, static_cast<int8_t*>(q), ldq, scale);
@@ -461,9 +462,7 @@ void launch_int8_few(const int8_t* A, long long lda, const float* a_scale, int M
                      const float* w_scale, int N, const float* bias, void* C, long long ldc, cudaStream_t st) {
   T_* c = static_cast<T_*>(C);
   const int blocks = ceil_div(N, 4 * kFewCols);
-  auto kernel = M == 1 ? gemm_int8_few_kernel<T_, 1>
-                       : M == 2 ? gemm_int8_few_kernel<T_, 2>
-                                : M <= 4 ? gemm_int8_few_kernel<T_, 4> : gemm_int8_few_kernel<T_, kFewRows>;
+  auto kernel = M == 1 ? gemm_int8_few_kernel<T_, 1> : M == 2 ? gemm_int8_few_kernel<T_, 2> : gemm_int8_few_kernel<T_, kFewRows>;
   kernel<<<blocks, 128, 0, st>>>(A, lda, a_scale, M, K, W, ldw, w_scale, N, bias, c, ldc);
 }
 
@@ -497,7 +496,8 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
       N <= 0 || M >= (1LL << 31))
     return MATE_ERR_ARG;
   if (!aligned16(A) || !aligned16(Wt) || !aligned16(C) || !aligned16(w_scale) || !aligned16(bias) ||
-      (reinterpret_cast<uintptr_t>(a_scale) & 3u) || !row_stride_ok(lda, K, 1) || !row_stride_ok(ldw, K, 1) || ldc < N)
+      (reinterpret_cast<uintptr_t>(a_scale) & 3u) || !row_stride_ok(lda, K, 1) || !row_stride_ok(ldw, K, 1) || ldc < N ||
+      ldc >= (1LL << 31))
     return MATE_ERR_ARG;
   if (K >= 131072) return MATE_ERR_UNSUPPORTED;
   t_launches = 0;
@@ -517,10 +517,21 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   p.M = static_cast<int>(M);
   p.N = N;
   p.K = K;
-  // the widest tile that still gives every pair of SMs one
+  // Tile width: 256, which feeds the MMAs best, unless there are fewer such tiles than pairs of SMs; then the one whose
+  // rounds over the pairs are the shortest (a tile costs its columns of W and a start).  16 x 2048 x 12288: 12.0 us at 256
+  // columns, 16.5 at 128, 21 at 64; 16 x 1024 x 4096: 8.7, 7.3 and 6.9.
   const int pairs_all = device_sms() / 2;
   p.bn = 256;
-  while (p.bn > 32 && (p.bn / 2 >= N || (long long)ceil_div(M, 256) * ceil_div(N, p.bn) < pairs_all)) p.bn /= 2;
+  if ((long long)ceil_div(M, 256) * ceil_div(N, 256) < pairs_all) {
+    long long best = 1LL << 62;
+    for (int bn = 256; bn >= 32; bn /= 2) {
+      const long long cost = (long long)ceil_div((long long)ceil_div(M, 256) * ceil_div(N, bn), pairs_all) * (bn + kI8TileStart);
+      if (cost < best) {
+        best = cost;
+        p.bn = bn;
+      }
+    }
+  }
   p.num_n_tiles = ceil_div(N, p.bn);
   const long long tiles = (long long)ceil_div(M, 256) * p.num_n_tiles;
   if (tiles >= (1LL << 31)) return MATE_ERR_SHAPE;
@@ -532,8 +543,9 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   p.ldc = ldc;
   p.vec = ldc * (out_dtype == MATE_BF16 ? 2 : 4) % 16 == 0;
   // Keep W in shared memory where that is the shorter way: its tiles take 1 / kI8KeepGain of the others' time, but the
-  // pairs share out whole column tiles.
-  constexpr double kI8KeepGain = 1.2;
+  // pairs share out whole column tiles.  65536 x 1024 x 4368 (64 tiles a pair against 63): 232 us against 256;
+  // 16384 x 1024 x 4096 (16 against 14): 65 against 59.
+  constexpr double kI8KeepGain = 1.1;
   const int mblocks = ceil_div(M, 256);
   int pairs = std::min(p.num_tiles, pairs_all);
   p.slots = std::min(p.num_n_tiles, pairs_all);

@@ -270,6 +270,18 @@ def test_gated_scan_in_parts(order, reverse):
     _close(h, *ref["h_last"], "f32", "h_last")
 
 
+@pytest.mark.parametrize("cfg", [SCAN[1], SCAN[7], SCAN[13]], ids=_scan_id)
+def test_gated_scan_state_in_place(cfg):
+    """The last state written over the first, as a stream of calls on one state buffer does, one chunk and several."""
+    x, g, _, kw = _scan_inputs(cfg, 17, True)
+    xd, gd, b, h0 = _dev(x, cfg.dtype), _dev(g, cfg.dtype), _dev(kw["bias"]), _dev(kw["h0"])
+    y, hl = M.gated_scan(xd, gd, cfg, bias=b, h0=h0)
+    for _ in range(5):
+        h = h0.clone()
+        y2, hl2 = M.gated_scan(xd, gd, cfg, bias=b, h0=h, h_last=h)
+        assert hl2 is h and torch.equal(y, y2) and torch.equal(hl, h)
+
+
 def test_gated_scan_gradient_against_differences():
     cfg = M.GatedScanConfig(B=2, T=7, H=3, W=5, D=8, order=3, dtype="f32")
     x, g, dy, kw = _scan_inputs(cfg, 8, True)
