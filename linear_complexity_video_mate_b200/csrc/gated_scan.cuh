@@ -29,7 +29,7 @@ constexpr int kGsThreads = 128, kGsBwdThreads = 256;   // 1 KB of a bf16 row per
 static_assert(kGsBatch == kGsState, "a state is saved before every batch of rows");
 constexpr int kGsMaxChunk = 128;
 constexpr int kGsOneChunk = 64;  // sequences up to this length are one chunk
-constexpr int kGsCarryCh = 16, kGsCarrySeg = 64;   // channels of a block of the carry kernel, runs of chunks it cuts them into
+constexpr int kGsCarryCh = 16, kGsCarrySeg = 64;   // the carry kernel: channels of a block, runs it cuts the chunks into
 
 // The grid rows of the steps s = 0, 1, .. of a recurrence: three nested counters, fastest first.
 struct GsOrder {

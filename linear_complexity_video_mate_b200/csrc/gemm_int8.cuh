@@ -315,7 +315,8 @@ __device__ __forceinline__ void mma_commit_both(uint64_t* bar) {
       : "memory");
 }
 
-// Tiled store from this CTA's shared memory (rows behind the matrix are left out); one thread issues it, and the source may be written again once tma_store_read() returns there.
+// Tiled store from this CTA's shared memory (rows behind the matrix are left out); one thread issues it, and the source
+// may be written again once tma_store_read() returns there.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),

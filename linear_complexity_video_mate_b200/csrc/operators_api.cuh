@@ -1,5 +1,5 @@
-// Host side of the operators beside the block: q/k norm with rotation, gated scan, 8-bit projection.  Included by mate_api.cu (it uses that
-// file's validation, trace and launch helpers).
+// Host side of the operators beside the block: q/k norm with rotation, gated scan, 8-bit projection.  Included by
+// mate_api.cu (it uses that file's validation, trace and launch helpers).
 #pragma once
 
 namespace {
@@ -462,7 +462,8 @@ void launch_int8_few(const int8_t* A, long long lda, const float* a_scale, int M
                      const float* w_scale, int N, const float* bias, void* C, long long ldc, cudaStream_t st) {
   T_* c = static_cast<T_*>(C);
   const int blocks = ceil_div(N, 4 * kFewCols);
-  auto kernel = M == 1 ? gemm_int8_few_kernel<T_, 1> : M == 2 ? gemm_int8_few_kernel<T_, 2> : gemm_int8_few_kernel<T_, kFewRows>;
+  auto kernel = M == 1   ? gemm_int8_few_kernel<T_, 1>
+                : M == 2 ? gemm_int8_few_kernel<T_, 2> : gemm_int8_few_kernel<T_, kFewRows>;
   kernel<<<blocks, 128, 0, st>>>(A, lda, a_scale, M, K, W, ldw, w_scale, N, bias, c, ldc);
 }
 
@@ -482,8 +483,9 @@ mate_status mate_quantize_rows(const void* x, long long ldx, long long M, int K,
   if (M == 0) return MATE_OK;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   trace_begin(MATE_K_QUANTIZE_ROWS, st);
-  if (dtype == MATE_BF16) launch_quantize(static_cast<const __nv_bfloat16*>(x), ldx, static_cast<int>(M), K, q, ldq, scale, st);
-  else launch_quantize(static_cast<const float*>(x), ldx, static_cast<int>(M), K, q, ldq, scale, st);
+  const int m = static_cast<int>(M);
+  if (dtype == MATE_BF16) launch_quantize(static_cast<const __nv_bfloat16*>(x), ldx, m, K, q, ldq, scale, st);
+  else launch_quantize(static_cast<const float*>(x), ldx, m, K, q, ldq, scale, st);
   MATE_LAUNCH_CHECK();
   return MATE_OK;
 }
@@ -525,7 +527,8 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   if ((long long)ceil_div(M, 256) * ceil_div(N, 256) < pairs_all) {
     long long best = 1LL << 62;
     for (int bn = 256; bn >= 32; bn /= 2) {
-      const long long cost = (long long)ceil_div((long long)ceil_div(M, 256) * ceil_div(N, bn), pairs_all) * (bn + kI8TileStart);
+      const long long tiles = (long long)ceil_div(M, 256) * ceil_div(N, bn);
+      const long long cost = (long long)ceil_div(tiles, pairs_all) * (bn + kI8TileStart);
       if (cost < best) {
         best = cost;
         p.bn = bn;

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(1024) sum_parts_kernel(const float* __restrict
 // How a lane's 16-byte units lie in a head and how their channels pair up.
 enum : int {
   kQkAdjacent = 0,   // 16 contiguous bytes; channels 2i, 2i + 1 pair up
-  kQkHalves = 1,     // 8 bytes of the first half of an axis' channels and the 8 bytes they pair with (r a multiple of 16 bytes)
+  kQkHalves = 1,     // 8 bytes of the first half of an axis' channels and the 8 they pair with (r a multiple of 16 bytes)
   kQkAny = 2         // 16 contiguous bytes, partners through shared memory (halves that 8-byte units do not divide)
 };
 
@@ -163,13 +163,14 @@ struct QkLane {
     }
   }
 
+  // (plain loads: the output may be the input)
   __device__ __forceinline__ uint4 load(const T_* head, int n) const {
     if constexpr (MODE == kQkHalves) {
-      const uint2 a = __ldg(reinterpret_cast<const uint2*>(head + c[n][0]));
-      const uint2 b = __ldg(reinterpret_cast<const uint2*>(head + c[n][1]));
+      const uint2 a = *reinterpret_cast<const uint2*>(head + c[n][0]);
+      const uint2 b = *reinterpret_cast<const uint2*>(head + c[n][1]);
       return make_uint4(a.x, a.y, b.x, b.y);
     } else {
-      return __ldg(reinterpret_cast<const uint4*>(head + c[n][0]));
+      return *reinterpret_cast<const uint4*>(head + c[n][0]);
     }
   }
   __device__ __forceinline__ void store(T_* head, int n, const float2 (&v)[P]) const {
@@ -268,7 +269,7 @@ __device__ __forceinline__ void qk_copy_v(const QkParams& p, const T_* src, T_* 
     uint4 u[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (v + j * step < nv) u[j] = __ldg(s + v + j * step);
+      if (v + j * step < nv) u[j] = s[v + j * step];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (v + j * step < nv) d[v + j * step] = u[j];

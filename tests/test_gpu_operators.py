@@ -24,7 +24,8 @@ def _host(rng, shape, dtype, scale=1.0):
 
 
 def _dev(a, dtype="f32"):
-    return torch.as_tensor(np.ascontiguousarray(a)).to(device="cuda", dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    return torch.as_tensor(np.ascontiguousarray(a)).to(device="cuda",
+                                                       dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
 
 
 def _np(t):
@@ -130,6 +131,32 @@ def test_qk_norm_rope_backward(cfg, weights):
     M.qk_norm_rope_backward(x, *dw, tabs, dview, cfg, dqkv=view)
     assert torch.equal(view.contiguous(), got["dqkv"])
     assert torch.isnan(big[:, :8]).all() and torch.isnan(big[:, 8 + cfg.width:]).all()
+
+
+# every way a head's channels lie over the lanes: lanes per head, two units per lane, pairs inside a lane or through
+# shared memory; more heads than one warp's share of a row
+QK_LANES = [M.QkConfig(B=1, T=2, H=3, W=2, hq=3, hk=2, hv=1, tp=tp, rt=r[0], rh=r[1], rw=r[2], pairing=pair, dtype=dt)
+            for dt, shapes in (("bf16", ((256, (88, 88, 80)), (256, (86, 84, 86)), (136, (48, 40, 48)), (32, (8, 8, 16)),
+                                         (32, (10, 10, 12)), (16, (8, 0, 8)))),
+                               ("f32", ((256, (88, 84, 84)), (256, (86, 84, 82)), (200, (68, 64, 60)), (132, (44, 40, 48)),
+                                        (64, (20, 20, 24)), (12, (4, 0, 4)), (12, (6, 2, 4)))))
+            for tp, r in shapes for pair in ("adjacent", "halves")]
+QK_LANES += [M.QkConfig(B=1, T=1, H=1, W=1, hq=40, hk=33, hv=5, tp=32, rt=32),
+             M.QkConfig(B=2, T=3, H=1, W=1, hq=1, hk=17, hv=2, tp=64, rt=6, pairing="halves")]
+
+
+@pytest.mark.parametrize("cfg", QK_LANES, ids=_qk_id)
+def test_qk_lane_layouts(cfg):
+    rng, qkv, (wq, wk), tabs, tabs_h = _qk_inputs(cfg, 18)
+    x, dw = _dev(qkv, cfg.dtype), [_dev(w) for w in (wq, wk)]
+    ref, bound = OP.qk_norm_rope(qkv, wq, wk, tabs_h, cfg)
+    _qk_check(M.qk_norm_rope(x, *dw, tabs, cfg), ref, bound, cfg, "out")
+    dout = _host(rng, (cfg.rows, cfg.width), cfg.dtype)
+    ref, bound, dws, dwb = OP.qk_norm_rope_backward(qkv, wq, wk, tabs_h, dout, cfg)
+    got = M.qk_norm_rope_backward(x, *dw, tabs, _dev(dout, cfg.dtype), cfg)
+    _qk_check(got["dqkv"], ref, bound, cfg, "dqkv")
+    _close(got["dwq"], dws[0], dwb[0], "f32", "dwq")
+    _close(got["dwk"], dws[1], dwb[1], "f32", "dwk")
 
 
 def test_qk_gradient_against_differences():
@@ -241,6 +268,55 @@ def test_gated_scan_extreme_gates(gate, spread, dtype):
     _scan_check(cfg, x, g, dy, kw)
 
 
+@pytest.mark.parametrize("B", [512, 128, 64])
+def test_gated_scan_long_chunks(B):
+    """Batches with so many channels that a thread walks 128, 64 or 32 rows: against the recurrence in 64 bits on the GPU,
+    with the bounds of the reference (oracle/operators.py)."""
+    cfg = M.GatedScanConfig(B=B, T=10, H=5, W=6, D=1024, order=1, reverse=True)
+    gen = torch.Generator(device="cuda").manual_seed(B)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    x, dy = (rnd(B, 300, 1024).bfloat16() for _ in range(2))
+    g, bias, h0, dhl = (rnd(B, 300, 1024) + 2).bfloat16(), rnd(1024), rnd(B, 1024), rnd(B, 1024)
+    states = M.gated_scan_states(cfg)
+    y, hl = M.gated_scan(x, g, cfg, bias=bias, h0=h0, states=states)
+    got = M.gated_scan_backward(x, g, states, dy, cfg, bias=bias, dh_last=dhl)
+    rows = torch.as_tensor(np.ascontiguousarray(OP.scan_rows(cfg))).cuda()
+    eps, worst = OP.EPS32, {}
+
+    def check(name, v, ref, bound, half):
+        tol = half * (ref.abs() + bound) + bound + 1e-37
+        worst[name] = max(worst.get(name, 0.0), ((v.double() - ref).abs() / tol).max().item())
+
+    h, mag, err = h0.double(), h0.double().abs(), torch.zeros_like(h0, dtype=torch.float64)
+    before = []
+    for r in rows:
+        z = g[:, r].double() + bias.double()
+        a, na, c = 1 / (1 + torch.exp(-z)), 1 / (1 + torch.exp(z)), (24 + 2 * z.abs()) * eps
+        before.append((h, mag, err, a, na, c))
+        h = a * h + na * x[:, r].double()
+        mag = a * mag + na * x[:, r].double().abs()
+        err = a * err + c * mag
+        check("y", y[:, r], h, err, OP.half_step("bf16"))
+    check("h_last", hl, h, err, OP.half_step("f32"))
+    lam, mag, err = dhl.double(), dhl.double().abs(), torch.zeros_like(h)
+    db, dbm = torch.zeros(1024, dtype=torch.float64, device="cuda"), torch.zeros(1024, dtype=torch.float64, device="cuda")
+    for r, (hb, hm, he, a, na, c) in zip(reversed(rows), reversed(before)):
+        d = dy[:, r].double()
+        l, ml, el = d + lam, d.abs() + mag, err + c * (d.abs() + mag)
+        check("dx", got["dx"][:, r], na * l, na * (el + c * ml), OP.half_step("bf16"))
+        xv, aa = x[:, r].double(), a * na
+        hx = hm + xv.abs()
+        dg, eg = l * (hb - xv) * aa, aa * (el * hx + ml * he + 2 * c * ml * hx)
+        check("dg", got["dg"][:, r], dg, eg, OP.half_step("bf16"))
+        db += dg.sum(0)
+        # 300 B terms in sums of at most 512 additions on any path
+        dbm += (eg + 512 * eps * aa * ml * hx).sum(0)
+        lam, mag, err = a * l, a * ml, a * (el + c * ml)
+    check("dh0", got["dh0"], lam, err, OP.half_step("f32"))
+    check("dbias", got["dbias"], db, dbm, OP.half_step("f32"))
+    assert all(v <= 1 for v in worst.values()), worst
+
+
 def test_gated_scan_infinite_gates():
     """A gate of -inf starts the state afresh from x, of +inf keeps it as it is, exactly."""
     cfg = M.GatedScanConfig(B=1, T=200, H=1, W=1, D=8, dtype="f32")
@@ -320,7 +396,8 @@ def test_quantize_rows_ties_and_edges():
     and largest values; rows with an infinity or NaN."""
     mid = np.arange(-126, 127) + 0.5
     rows = [np.concatenate([mid, [127.0, -127.0, 0.0]])]
-    rows += [np.concatenate([np.nextafter(mid.astype(np.float32), np.float32(to)), [127.0, -127.0, 0.0]]) for to in (-200, 200)]
+    rows += [np.concatenate([np.nextafter(mid.astype(np.float32), np.float32(to)), [127.0, -127.0, 0.0]])
+             for to in (-200, 200)]
     rows += [r * np.float32(2.0 ** e) for r in rows for e in (-100, -20, 3, 100)]
     rows += [r * np.float32(1.37) for r in rows[:3]]
     rows += [np.zeros(256), np.full(256, 1e-45), np.linspace(-3e-44, 3e-44, 256), np.linspace(-1e-38, 1e-38, 256),
@@ -336,9 +413,10 @@ def test_quantize_rows_ties_and_edges():
     np.testing.assert_array_equal(q.cpu().numpy(), ref_q)
 
 
-INT8 = [(1, 16, 1), (1, 1024, 96), (2, 2048, 1001), (5, 100, 37), (8, 4096, 4096), (9, 1040, 513), (16, 512, 264), (17, 256, 256),
-        (64, 333, 2048), (129, 128, 255), (257, 144, 288), (300, 1024, 1000), (513, 2048, 520), (1000, 80, 4368),
-        (2000, 1024, 300), (600, 48, 19240), (10000, 250, 600), (4000, 1025, 777)]
+INT8 = [(1, 16, 1), (1, 1024, 96), (2, 2048, 1001), (5, 100, 37), (8, 4096, 4096), (9, 1040, 513), (16, 512, 264),
+        (17, 256, 256), (64, 333, 2048), (129, 128, 255), (257, 144, 288), (300, 1024, 1000), (513, 2048, 520), (1000, 80, 4368),
+        (2000, 1024, 300), (600, 48, 19240), (10000, 250, 600), (4000, 1025, 777), (4, 4096, 100), (3, 31, 9),
+        (16, 1024, 6000), (40, 4096, 70)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
