@@ -29,7 +29,7 @@ constexpr int kGsThreads = 128, kGsBwdThreads = 256;   // 1 KB of a bf16 row per
 static_assert(kGsBatch == kGsState, "a state is saved before every batch of rows");
 constexpr int kGsMaxChunk = 128;
 constexpr int kGsOneChunk = 64;  // sequences up to this length are one chunk
-constexpr int kGsCarryCh = 16, kGsCarrySeg = 64;   // the carry kernel: channels of a block, runs it cuts the chunks into
+constexpr int kGsCarryHeld = 8;  // pairs that a thread of the carry kernel holds
 
 // The grid rows of the steps s = 0, 1, .. of a recurrence: three nested counters, fastest first.
 struct GsOrder {
@@ -308,35 +308,53 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : 8) gated_adj
 }
 
 // carry [chunks][cols] (cols = B D) from the pairs: the start value (null: 0) carried over the chunks, `back`: from the
-// last chunk to the first.  A block takes kGsCarryCh columns; each of its kGsCarrySeg threads per column joins a run of
-// chunks, then the runs before it in order, then walks its run again.  Latency: 10 us for 2048 chunks of 1024 columns.
-__global__ void __launch_bounds__(kGsCarryCh * kGsCarrySeg)
+// last chunk to the first.  A block takes CH columns; each of its SEG threads per column joins a run of chunks, then the
+// runs before it in order, then walks its run again.  Latency bounds it, so the runs are as many as give a thread eight
+// chunks or so (8 samples of 112 chunks, 512 columns: a scan of 18.6 us with 32 runs, 22.0 with 64, 31.9 with 128).
+template <int CH, int SEG>
+__global__ void __launch_bounds__(CH * SEG)
     gated_carry_kernel(const float2* __restrict__ pair, const float* __restrict__ start, float* __restrict__ carry,
                        int chunks, int cols, int back) {
-  __shared__ float2 s[kGsCarrySeg][kGsCarryCh];
-  const int lc = threadIdx.x % kGsCarryCh, seg = threadIdx.x / kGsCarryCh, c = blockIdx.x * kGsCarryCh + lc;
-  const int len = (chunks + kGsCarrySeg - 1) / kGsCarrySeg, k0 = min(seg * len, chunks), k1 = min(k0 + len, chunks);
+  __shared__ float2 s[SEG][CH];
+  const int lc = threadIdx.x % CH, seg = threadIdx.x / CH, c = blockIdx.x * CH + lc;
+  const int len = (chunks + SEG - 1) / SEG, k0 = min(seg * len, chunks), k1 = min(k0 + len, chunks);
   const bool live = c < cols;
+  auto at = [&](int k) { return (long long)(back ? chunks - 1 - k : k) * cols + c; };
+  float2 v[kGsCarryHeld];   // the run's first pairs, held for the second walk
   float A = 1.f, H = 0.f;
   if (live) {
+#pragma unroll
+    for (int j = 0; j < kGsCarryHeld; ++j) v[j] = k0 + j < k1 ? pair[at(k0 + j)] : make_float2(1.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < kGsCarryHeld; ++j) {
+      H = fmaf(v[j].x, H, v[j].y);
+      A *= v[j].x;
+    }
 #pragma unroll 8
-    for (int k = k0; k < k1; ++k) {
-      const float2 v = __ldg(pair + (long long)(back ? chunks - 1 - k : k) * cols + c);
-      H = fmaf(v.x, H, v.y);
-      A *= v.x;
+    for (int k = k0 + kGsCarryHeld; k < k1; ++k) {
+      const float2 u = pair[at(k)];
+      H = fmaf(u.x, H, u.y);
+      A *= u.x;
     }
   }
   s[seg][lc] = make_float2(A, H);
+  const float h0 = live && start != nullptr ? start[c] : 0.f;
   __syncthreads();
   if (!live) return;
-  float h = start != nullptr ? start[c] : 0.f;
-  for (int q = 0; q < seg; ++q) h = fmaf(s[q][lc].x, h, s[q][lc].y);
+  float h = h0;
 #pragma unroll 8
-  for (int k = k0; k < k1; ++k) {
-    const long long at = (long long)(back ? chunks - 1 - k : k) * cols + c;
-    carry[at] = h;
-    const float2 v = __ldg(pair + at);
-    h = fmaf(v.x, h, v.y);
+  for (int q = 0; q < seg; ++q) h = fmaf(s[q][lc].x, h, s[q][lc].y);
+#pragma unroll
+  for (int j = 0; j < kGsCarryHeld; ++j)
+    if (k0 + j < k1) {
+      carry[at(k0 + j)] = h;
+      h = fmaf(v[j].x, h, v[j].y);
+    }
+#pragma unroll 8
+  for (int k = k0 + kGsCarryHeld; k < k1; ++k) {
+    carry[at(k)] = h;
+    const float2 u = pair[at(k)];
+    h = fmaf(u.x, h, u.y);
   }
 }
 

@@ -288,8 +288,12 @@ int gated_blocks(GatedScanParams* p, int np, int threads) {
 mate_status launch_carry(const GatedScanParams& p, const float* start, int back, cudaStream_t st) {
   const int cols = static_cast<int>(p.B.d) * p.D;
   trace_begin(MATE_K_GATED_SCAN_CARRY, st);
-  gated_carry_kernel<<<ceil_div(cols, kGsCarryCh), kGsCarryCh * kGsCarrySeg, 0, st>>>(p.pair, start, p.carry, p.chunks,
-                                                                                      cols, back);
+  if (p.chunks <= 8 * kGsCarryHeld)
+    gated_carry_kernel<32, 8><<<ceil_div(cols, 32), 256, 0, st>>>(p.pair, start, p.carry, p.chunks, cols, back);
+  else if (p.chunks <= 32 * kGsCarryHeld)
+    gated_carry_kernel<16, 32><<<ceil_div(cols, 16), 512, 0, st>>>(p.pair, start, p.carry, p.chunks, cols, back);
+  else
+    gated_carry_kernel<8, 64><<<ceil_div(cols, 8), 512, 0, st>>>(p.pair, start, p.carry, p.chunks, cols, back);
   MATE_LAUNCH_CHECK();
   return MATE_OK;
 }

@@ -203,6 +203,7 @@ SCAN = [
     M.GatedScanConfig(B=2, T=9, H=13, W=5, D=44, order=3, reverse=True, dtype="f32"),
     M.GatedScanConfig(B=1, T=33, H=8, W=8, D=132, order=2, dtype="f32"),
     M.GatedScanConfig(B=3, T=64, H=2, W=1, D=128, order=1, dtype="f32"),
+    M.GatedScanConfig(B=1, T=9001, H=1, W=1, D=12, dtype="f32"),
 ]
 
 
