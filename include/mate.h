@@ -502,7 +502,7 @@ MATE_API mate_status mate_gated_scan_backward(const void* x, long long ldx, cons
  * mate_project_int8: C[m, n] = (sum_k A[m, k] W[n, k]) a_scale[m] w_scale[n] + bias[n], the sum exact in 32 bits,
  * the rest in fp32, rounded once to out_dtype.  A [M, K] and Wt [N, K] int8 (row strides lda, ldw, multiples of 16,
  * any K < 131072), a_scale [M], w_scale [N], bias [N] (null: none) float, C [M, N] (row stride ldc >= N elements).
- * M = 0 does nothing.
+ * M = 0 does nothing; M, N and mate_quantize_rows' K are at most 2^31 - 2^14.
  */
 MATE_API mate_status mate_quantize_rows(const void* x, long long ldx, long long M, int K, mate_dtype dtype, void* q,
                                         long long ldq, float* scale, mate_stream_t stream);

@@ -414,6 +414,10 @@ mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g
 // ------------------------------------------------------------------------------ 8-bit projection
 namespace {
 
+// Rows and columns are counted in 32 bits, and the kernels step past the last one by up to a grid's share of rows (8 blocks
+// of 8 rows on every SM) or a tile's of columns before they compare: the sizes stay that far below 2^31.
+constexpr long long kI8MaxSize = (1LL << 31) - (1LL << 14);
+
 // 2D matrix of bytes [rows, cols], row stride ld (a multiple of 16); box = box_rows x 128 columns, 128B swizzle.
 // Columns and rows behind the matrix read zeros.
 bool make_tmap_s8(CUtensorMap* m, const void* ptr, long long rows, long long cols, long long ld, int box_rows) {
@@ -479,7 +483,8 @@ mate_status mate_quantize_rows(const void* x, long long ldx, long long M, int K,
                                long long ldq, float* scale, mate_stream_t stream) {
   if (dtype != MATE_BF16 && dtype != MATE_F32) return MATE_ERR_ARG;
   const int es = dtype == MATE_BF16 ? 2 : 4;
-  if (x == nullptr || q == nullptr || scale == nullptr || M < 0 || K <= 0 || M >= (1LL << 31)) return MATE_ERR_ARG;
+  if (x == nullptr || q == nullptr || scale == nullptr || M < 0 || K <= 0 || M > kI8MaxSize || K > kI8MaxSize)
+    return MATE_ERR_ARG;
   if (!aligned16(x) || !aligned16(q) || (reinterpret_cast<uintptr_t>(scale) & 3u) || !row_stride_ok(ldx, K, es) ||
       !row_stride_ok(ldq, K, 1))
     return MATE_ERR_ARG;
@@ -499,7 +504,7 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
                               mate_dtype out_dtype, mate_stream_t stream) {
   if (out_dtype != MATE_BF16 && out_dtype != MATE_F32) return MATE_ERR_ARG;
   if (A == nullptr || a_scale == nullptr || Wt == nullptr || w_scale == nullptr || C == nullptr || M < 0 || K <= 0 ||
-      N <= 0 || M >= (1LL << 31))
+      N <= 0 || M > kI8MaxSize || N > kI8MaxSize)
     return MATE_ERR_ARG;
   if (!aligned16(A) || !aligned16(Wt) || !aligned16(C) || !aligned16(w_scale) || !aligned16(bias) ||
       (reinterpret_cast<uintptr_t>(a_scale) & 3u) || !row_stride_ok(lda, K, 1) || !row_stride_ok(ldw, K, 1) || ldc < N ||

@@ -115,6 +115,19 @@ def test_int8_argument_refusals(lib):
         (dict(M=0), OK)])
 
 
+def test_int8_sizes_next_to_the_index_range(lib):
+    """Row and column counters are 32-bit and run past the last row or column before they are compared: sizes that leave
+    them no room below 2^31 are refused (one more than the documented most; the largest a caller can pass)."""
+    most, top = (1 << 31) - (1 << 14), (1 << 31) - 16
+    for n in (most + 1, (1 << 31) - 9472, (1 << 31) - 256, (1 << 31) - 1):
+        for dt in (0, 1):
+            assert lib.mate_quantize_rows(F, 16, n, 8, dt, 2 * F, 16, F, None) == ARG, n
+            assert lib.mate_project_int8(F, 16, F, n, 16, 2 * F, 16, F, 32, None, 3 * F, 32, dt, None) == ARG, n
+            assert lib.mate_project_int8(F, 16, F, 4, 16, 2 * F, 16, F, n, None, 3 * F, (1 << 31) - 1, dt, None) == ARG, n
+    for k in (most + 1, (1 << 31) - 256, top):
+        assert lib.mate_quantize_rows(F, top, 1, k, 0, 2 * F, top, F, None) == ARG, k
+
+
 def test_binding_refusals():
     """The Python layer names the argument: wrong type, shape, place or stride (CPU tensors stand in)."""
     cfg = M.QkConfig(B=1, T=2, H=1, W=1, hq=1, hk=1, hv=1, tp=16)
