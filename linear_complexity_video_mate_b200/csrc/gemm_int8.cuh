@@ -391,7 +391,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
         const int n_mma = min(p.bn, (p.N - w.nb * p.bn + 31) & ~31);
         const int row_w = w.nb * p.bn + rank * (n_mma / 2);
         if (w.column_starts()) {
-          if (!mbar_wait(kempty, kphase ^ 1)) break;
+          if (!mbar_wait(kempty, kphase ^ 1)) { ok = false; break; }
           kphase ^= 1;
           if (leader) mbar_arrive_expect_tx(kfull, 2 * nk * (p.bn / 2) * 128);
           for (int kb = 0; kb < nk; ++kb)
@@ -407,6 +407,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kI8Threads, 1)
           if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
         }
       }
+      // the last arrivals of every stage and of the kept columns come from the leader's commits, in this CTA's shared
+      // memory: it does not leave before they are in (a stage or columns never used: the wait passes at once)
+      for (int s = 0; ok && s < p.stages; ++s) {
+        ok = mbar_wait(&empty[stage], phase ^ 1);
+        if (++stage == (uint32_t)p.stages) { stage = 0; phase ^= 1; }
+      }
+      if (KEEP && ok) mbar_wait(kempty, kphase ^ 1);
     }
   } else if (warp == 1) {
     if (leader && lane == 0) {

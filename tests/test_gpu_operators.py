@@ -444,6 +444,47 @@ def test_project_int8(M_, K, N, dtype):
     assert M.device_status() == 0
 
 
+def _int8_rule(M_, K, N):
+    """(tile columns, whether W's column tiles are kept in shared memory) that the library's rule gives on this GPU."""
+    up = lambda a, b: -(-a // b)
+    pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
+    mb, bn = up(M_, 256), 256
+    if mb * up(N, 256) < pairs:
+        bn = min((256, 128, 64, 32), key=lambda b: up(mb * up(N, b), pairs) * (b + 32))
+    nt = up(N, bn)
+    slots = min(nt, pairs)
+    groups = min(pairs // slots, mb)
+    return bn, K <= 1024 and bn == 256 and up(nt, slots) * up(mb, groups) < 1.1 * up(mb * nt, min(mb * nt, pairs))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M_,K,N", [(65536, 1024, 512),   # 7 row tiles a pair, the ring of A wraps, accumulators reused
+                                    (20000, 1000, 600),   # the last block of K and the last tiles cut
+                                    (512, 144, 37888),    # a second column tile over the first
+                                    (512, 1000, 56700)])  # a third one, cut, with more blocks of K than the ring holds
+def test_project_int8_kept_weights(M_, K, N, dtype):
+    """W kept in shared memory while a pair walks down the rows: reused accumulators and ring stages, column tiles loaded
+    over earlier ones; launch after launch, since a CTA may not leave before its last arrivals are in."""
+    assert _int8_rule(M_, K, N) == (256, True)
+    gen = torch.Generator(device="cuda").manual_seed(M_ + K)
+    ints = lambda r: torch.randint(-128, 128, (r, (K + 15) // 16 * 16), generator=gen, device="cuda", dtype=torch.int8)[:, :K]
+    A, W = ints(M_), ints(N)
+    sa, sw = ((0.5 + torch.rand(n, generator=gen, device="cuda")) / 127 for n in (M_, N))
+    bias = torch.randn(N, generator=gen, device="cuda")
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    outs = [M.project_int8(A, sa, W, sw, bias=bias, out_dtype=dt) for _ in range(4)]
+    again = outs[1]
+    for _ in range(20):
+        M.project_int8(A, sa, W, sw, bias=bias, out=again)
+    assert M.device_status() == 0
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
+    for r in range(0, M_, 8192):   # integers below 2^53 add up exactly in 64 bits
+        v = (A[r:r + 8192].double() @ W.double().t()) * sa[r:r + 8192, None].double() * sw.double()
+        ref, bound = v + bias.double(), 4 * OP.EPS32 * (v.abs() + bias.double().abs())
+        tol = OP.half_step(dtype) * (ref.abs() + bound) + bound
+        assert ((outs[0][r:r + 8192].double() - ref).abs() <= tol).all(), r
+
+
 def test_project_int8_largest_sums():
     """The longest K with all products at their largest: the sum stays exact in 32 bits (2^31 - 16384)."""
     K = 131071
