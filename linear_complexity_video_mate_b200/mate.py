@@ -425,8 +425,15 @@ def _keep(obj, **values):
         object.__setattr__(obj, k, v)
 
 
+class _Config:
+    """Copies and pickles go by the fields: the C structure and the pointer to it are made anew."""
+
+    def __reduce__(self):
+        return type(self), tuple(getattr(self, f.name) for f in dataclasses.fields(self))
+
+
 @dataclasses.dataclass(frozen=True)
-class QkConfig:
+class QkConfig(_Config):
     """Shape of qk_norm_rope's rows: B samples of T x H x W tokens, hq query, hk key and hv value heads of tp channels
     (tesa_forward's rows: all three th); rt / rh / rw of a head's first channels turn with the token's t / h / w
     position, in pairs of "adjacent" channels or of the "halves" of each axis' channels."""
@@ -528,7 +535,7 @@ def qk_norm_rope_backward(qkv: torch.Tensor, wq: Optional[torch.Tensor], wk: Opt
 
 
 @dataclasses.dataclass(frozen=True)
-class GatedScanConfig:
+class GatedScanConfig(_Config):
     """Shape of gated_scan: B samples of T x H x W tokens with D channels, walked along scan order `order` (as
     rms_permute), from its last position back if `reverse`."""
 

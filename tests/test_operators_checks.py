@@ -1,5 +1,7 @@
 """Host-side checks of the operators beside the block (no GPU): every refusal comes before any device work."""
+import copy
 import ctypes
+import pickle
 
 import numpy as np
 import pytest
@@ -153,6 +155,19 @@ def test_binding_refusals():
         M.GatedScanConfig(B=1, T=2, H=1, W=1, D=16, dtype="f16")
     with pytest.raises(ValueError, match="T ="):
         M.GatedScanConfig(B=1, T=1 << 32, H=1, W=1, D=16)
+
+
+@pytest.mark.parametrize("cfg", [
+    M.QkConfig(B=1, T=2, H=3, W=4, hq=5, hk=2, hv=2, tp=128, rt=32, rh=48, rw=48, pairing="halves", eps=1e-5, dtype="f32"),
+    M.GatedScanConfig(B=2, T=300, H=4, W=5, D=64, order=3, reverse=True, dtype="f32")], ids=["qk", "scan"])
+def test_configs_copy_and_pickle(lib, cfg):
+    """A module that holds a configuration can be copied, saved and sent to another process: before and after its cached
+    sizes were asked for."""
+    for _ in range(2):
+        for c in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg)), copy.deepcopy([cfg, cfg])[1]):
+            assert c == cfg and hash(c) == hash(cfg) and bytes(c.ccfg) == bytes(cfg.ccfg)
+            assert c.ref._obj is c.ccfg and c.ccfg is not cfg.ccfg and (c.rows, c.tdtype) == (cfg.rows, cfg.tdtype)
+            assert c.backward_workspace_bytes == cfg.backward_workspace_bytes > 0
 
 
 # -------------------------------------------------------------------------------- pins of the fp64 reference
