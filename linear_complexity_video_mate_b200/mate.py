@@ -410,13 +410,16 @@ def _workspace(ws: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> O
     return ws
 
 
+def _int(value, name: str, bits: int = 32) -> int:
+    """The value as an integer of the C interface (one that does not fit is refused, not cut)."""
+    v = int(value)
+    if not -(1 << bits - 1) <= v < (1 << bits - 1):
+        raise ValueError(f"{name} = {v} does not fit a {bits}-bit int")
+    return v
+
+
 def _ints(obj, names):
-    """The attributes as C ints (a value that does not fit is refused, not cut)."""
-    vals = [int(getattr(obj, k)) for k in names]
-    for k, v in zip(names, vals):
-        if not -(1 << 31) <= v < (1 << 31):
-            raise ValueError(f"{k} = {v} does not fit a 32-bit int")
-    return vals
+    return [_int(getattr(obj, k), k) for k in names]
 
 
 def _keep(obj, **values):
@@ -470,11 +473,12 @@ class QkConfig(_Config):
 def rope_table(count: int, dims: int, start: int = 0, theta: float = 10000.0, device="cuda",
                stream=None) -> torch.Tensor:
     """[count, dims / 2, 2] fp32: (cos, sin) of (start + p) theta^(-2 i / dims), the angle in 64 bits (made once)."""
+    count, dims, start = _int(count, "count"), _int(dims, "dims"), _int(start, "start", 64)
     index = _device_index(device)
     with _on(index, stream):
-        tab = torch.empty((max(int(count), 0), max(int(dims), 0) // 2, 2), dtype=torch.float32, device=f"cuda:{index}")
-        st = 0 if dims == 0 else _lib.load().mate_rope_table(tab.data_ptr(), int(start), int(count), int(dims),
-                                                             float(theta), _raw_stream(index))
+        tab = torch.empty((max(count, 0), max(dims, 0) // 2, 2), dtype=torch.float32, device=f"cuda:{index}")
+        st = 0 if dims == 0 else _lib.load().mate_rope_table(tab.data_ptr(), start, count, dims, float(theta),
+                                                             _raw_stream(index))
     _lib.check(st, "mate_rope_table")
     return tab
 
@@ -647,6 +651,7 @@ def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Opti
     if x.dim() != 2:
         raise ValueError(f"x: expected [M, K], got {tuple(x.shape)}")
     (M, K), index, code = x.shape, x.get_device(), _mate_dtype(x.dtype, "x")
+    _int(K, "K")
     ldx = _rows(x, x.dtype, M, K, index, "x")
     with _on(index, stream):
         if q is None:
@@ -671,6 +676,8 @@ def project_int8(A: torch.Tensor, a_scale: torch.Tensor, Wt: torch.Tensor, w_sca
     if A.dim() != 2 or Wt.dim() != 2:
         raise ValueError(f"A and Wt: expected [M, K] and [N, K], got {tuple(A.shape)} and {tuple(Wt.shape)}")
     (M, K), N, index, f32 = A.shape, Wt.shape[0], A.get_device(), torch.float32
+    _int(K, "K")
+    _int(N, "N")
     lda = _rows(A, torch.int8, M, K, index, "A")
     ldw = _rows(Wt, torch.int8, N, K, index, "Wt")
     with _on(index, stream):

@@ -157,6 +157,24 @@ def test_binding_refusals():
         M.GatedScanConfig(B=1, T=1 << 32, H=1, W=1, D=16)
 
 
+def test_binding_sizes_are_not_cut():
+    """Sizes of 2^32 and a little fit a 64-bit tensor, not the library's ints: refused, where cut to 32 bits they would be
+    a small job that leaves most of the output unwritten (expanded CPU tensors stand in)."""
+    wide = lambda rows, cols, dtype: torch.zeros((1, 1), dtype=dtype).expand(rows, cols)
+    big = (1 << 32) + 16
+    with pytest.raises(ValueError, match="K = "):
+        M.quantize_rows(wide(2, big, torch.bfloat16))
+    s = torch.zeros(1)
+    with pytest.raises(ValueError, match="K = "):
+        M.project_int8(wide(2, big, torch.int8), s, wide(2, big, torch.int8), s)
+    with pytest.raises(ValueError, match="N = "):
+        M.project_int8(wide(2, 16, torch.int8), s, wide(big, 16, torch.int8), s)
+    for kw, name in ((dict(count=big, dims=2), "count"), (dict(count=2, dims=big), "dims"),
+                     (dict(count=2, dims=2, start=(1 << 64) + 5), "start"), (dict(count=2, dims=2, start=-(1 << 63) - 1), "start")):
+        with pytest.raises(ValueError, match=f"{name} = "):
+            M.rope_table(**kw, device="cuda:0")
+
+
 @pytest.mark.parametrize("cfg", [
     M.QkConfig(B=1, T=2, H=3, W=4, hq=5, hk=2, hv=2, tp=128, rt=32, rh=48, rw=48, pairing="halves", eps=1e-5, dtype="f32"),
     M.GatedScanConfig(B=2, T=300, H=4, W=5, D=64, order=3, reverse=True, dtype="f32")], ids=["qk", "scan"])
