@@ -16,8 +16,10 @@ namespace mate {
 // 127 * 2^-23, so k from t (by adding 1.5 * 2^23, which leaves k in the sum's low byte) is right or the neighbour of the
 // right one; the remainder x - k s, which one fma gives without error (it has at most as many bits as x where k is in
 // doubt), tells: beyond s / 2, k is one off.  Where the remainder is just s / 2, t decides alone: TIES looks at those, too.
-// bf16 rows need that only if s has few bits (quant_ties), and quotients near midpoints are common there (x and the row's
-// maximum are ratios of small integers), so the correction has no branch.
+// bf16 rows never need that.  A bf16 x is (k + 1/2) s only if s has at most 8 significant bits; s is the row's maximum, an
+// integer p of 8 bits times 2^e, over 127, and p / 127 lies within 2^-24 of such a number only for p = 127 and 254: a power
+// of two, whose reciprocal, and with it t, is exact.  Quotients near midpoints are common there (x and the row's maximum
+// are ratios of small integers), so the correction has no branch.
 template <bool TIES>
 __device__ __forceinline__ float2 quant_two(float2 x, float inv, float s, float hs) {
   float2 m = add2(mul_f32x2(x, both(inv)), both(12582912.f));
@@ -38,13 +40,6 @@ __device__ __forceinline__ uint32_t quant_bytes(float2 lo, float2 hi) {
 __device__ __forceinline__ int8_t quant_one(float x, float inv, float s, float hs) {
   return static_cast<int8_t>(__float_as_uint(quant_two<true>(make_float2(x, 0.f), inv, s, hs).x));
 }
-// Whether a bf16 x can be (k + 1/2) s with t inexact: s has at most 8 significant bits and is no power of two (whose
-// reciprocal, and with it t, is exact).
-__device__ __forceinline__ bool quant_ties(float s) {
-  const uint32_t m = __float_as_uint(s) & 0x7fffffu;
-  return (m & 0xffffu) == 0 && m != 0;
-}
-
 constexpr float kQuantTiny = 1e-30f;   // scales below: 1 / s may overflow, the quotient is formed in 64 bits
 
 __device__ __forceinline__ int quant_round_tiny(float x, float s) {
@@ -123,11 +118,11 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T_* __restrict
     const float s = bad ? __uint_as_float(0x7fc00000u) : __uint_as_float(mx) / 127.f;
     if (t == 0) scale[r] = s;
     const float inv = 1.f / s, hs = 0.5f * s;
-    if (bad || s < kQuantTiny || (sizeof(T_) == 2 && quant_ties(s))) {   // rare
+    if (bad || s < kQuantTiny) {   // rare
 #pragma unroll 1
       for (int c = t; c < K; c += G) {
         const float v = to_f32(xr[c]);
-        qr[c] = bad ? 0 : s < kQuantTiny ? static_cast<int8_t>(quant_round_tiny(v, s)) : quant_one(v, inv, s, hs);
+        qr[c] = bad ? 0 : static_cast<int8_t>(quant_round_tiny(v, s));
       }
       continue;
     }

@@ -414,6 +414,68 @@ def test_quantize_rows_ties_and_edges():
     np.testing.assert_array_equal(q.cpu().numpy(), ref_q)
 
 
+def _quantised(x):
+    """(q, scale) of OP.quantize_rows on the GPU: a quotient in 64 bits rounds to 32, or to an integer, as the exact one
+    does, since one that is no midpoint of them is 2^-34 of itself or more away from it."""
+    scale = (x.abs().amax(1).double() / 127).float()
+    q = torch.round(x.double() / scale.double()[:, None]).nan_to_num(0)
+    return q.clamp(-127, 127).to(torch.int8), scale
+
+
+# per type: lengths that a warp holds as 1, 2, 4 and 8 vectors a lane, odd ones among them
+WARP_ROWS = {"bf16": (249, 256, 257, 512, 1021, 1024, 2041, 2048), "f32": (125, 128, 255, 256, 511, 512, 1023, 1024)}
+
+
+@pytest.mark.parametrize("dtype,K", [(d, k) for d in WARP_ROWS for k in WARP_ROWS[d]])
+@pytest.mark.parametrize("M_", [901, 20011])
+def test_quantize_many_rows(M_, K, dtype):
+    """A warp per row, one row or several each."""
+    assert M_ >= 6 * torch.cuda.get_device_properties(0).multi_processor_count
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(M_, (K + 7) // 8 * 8, generator=gen, device="cuda") * torch.exp2(
+        torch.randint(-30, 30, (M_, 1), generator=gen, device="cuda").float())
+    x = (x.bfloat16() if dtype == "bf16" else x)[:, :K]
+    x[7] = 0
+    ref_q, ref_s = _quantised(x.contiguous())
+    big = torch.full((M_, (K + 15) // 16 * 16 + 16), 77, dtype=torch.int8, device="cuda")
+    q, s = M.quantize_rows(x, q=big[:, :K])
+    assert torch.equal(s, ref_s) and torch.equal(q, ref_q) and (big[:, K:] == 77).all()
+
+
+@pytest.mark.parametrize("dtype,K", [("bf16", 2056), ("bf16", 4801), ("bf16", 12000), ("bf16", 16500),
+                                     ("f32", 1028), ("f32", 2303), ("f32", 6000), ("f32", 8300)])
+def test_quantize_blocks_of_several_rows(dtype, K):
+    """Rows too long for a warp, more of them than blocks."""
+    M_ = 8 * torch.cuda.get_device_properties(0).multi_processor_count + 333
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.randn(M_, (K + 7) // 8 * 8, generator=gen, device="cuda") * (1 + torch.arange(M_, device="cuda") % 5)[:, None]
+    x = (x.bfloat16() if dtype == "bf16" else x)[:, :K]
+    q, s = M.quantize_rows(x)
+    ref_q, ref_s = _quantised(x)
+    assert torch.equal(s, ref_s) and torch.equal(q, ref_q)
+
+
+@pytest.mark.parametrize("few", [True, False])
+def test_quantize_bf16_midpoints(few):
+    """Every bf16 row maximum, with all midpoints of the integers' multiples and their bf16 neighbours: rows of a few and of
+    many (a block and a warp per row).  Exact midpoints need a scale that is a power of two (maxima 127 * 2^e)."""
+    top = torch.arange(1, 0x7f80, dtype=torch.int32, device="cuda").to(torch.int16).view(torch.bfloat16)
+    if few:
+        top = torch.cat((top[::97], 127 * torch.exp2(torch.arange(-90, 90, 9, device="cuda")).bfloat16()))[:880]
+    mid = torch.arange(-126, 126, device="cuda") + 0.5
+    near = ((top.double() / 127)[:, None] * mid).bfloat16()
+    step = near.view(torch.int16)
+    x = torch.cat([top[:, None], near, (step - 1).view(torch.bfloat16), (step + 1).view(torch.bfloat16)], dim=1)
+    # the tiniest rows' midpoints round to 0 and to the maximum: neighbours that leave the row's range are left out
+    x = torch.where(x.abs() <= top[:, None], x, torch.zeros_like(x))
+    x = torch.nn.functional.pad(x, (0, -x.shape[1] % 8))
+    ref_q, ref_s = _quantised(x)
+    q, s = M.quantize_rows(x)
+    assert torch.equal(s, ref_s) and torch.equal(q, ref_q)
+    exact = (x.double() / ref_s.double()[:, None] % 1 == 0.5).any(1)
+    assert exact.any() and (few or len(x) >= 6 * torch.cuda.get_device_properties(0).multi_processor_count)
+
+
 INT8 = [(1, 16, 1), (1, 1024, 96), (2, 2048, 1001), (5, 100, 37), (8, 4096, 4096), (9, 1040, 513), (16, 512, 264),
         (17, 256, 256), (64, 333, 2048), (129, 128, 255), (257, 144, 288), (300, 1024, 1000), (513, 2048, 520), (1000, 80, 4368),
         (2000, 1024, 300), (600, 48, 19240), (10000, 250, 600), (4000, 1025, 777), (4, 4096, 100), (3, 31, 9),
