@@ -100,9 +100,15 @@ struct GsWalk {
   }
 };
 
-// a = sigmoid(z) and 1 - a, each to full precision, from t = -z log2 e: with e = 2^t, a = 1 / (1 + e) (0 where that is
-// below the normal numbers), and 1 - a is e a where a is above 1/2, the difference where it is not (there e a may be
-// infinity times 0).  NaN stays NaN.
+// The gate's argument, t = -z log2 e.  g and the bias are added first: scaled first, each by itself, the bias would leave
+// its own rounding (27 half steps at g = 60, bias = -55) where the two cancel.
+constexpr float kGsLog2e = -1.4426950408889634f;
+__device__ __forceinline__ float2 gs_arg(float2 g, float2 bias) { return mul_f32x2(add2(g, bias), both(kGsLog2e)); }
+
+// a = sigmoid(z) and 1 - a, each to its own size: with e = 2^t, a = 1 / (1 + e) (0 where that is below the normal numbers),
+// and 1 - a is e a where a is above 1/2, the difference where it is not (there e a may be infinity times 0).  The argument's
+// three roundings (the sum, the product, the constant) move the smaller of the two by up to 2.2 |z| half steps, the special
+// functions add a few.  NaN stays NaN.
 __device__ __forceinline__ float2 gs_keep(float2 t, float2* e) {
   *e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
   const float2 d = add2(*e, both(1.f));
@@ -118,7 +124,6 @@ __device__ __forceinline__ void gs_gate(float2 t, float2* a, float2* na) {
   na->x = t.x < 0.f ? p.x : q.x;
   na->y = t.y < 0.f ? p.y : q.y;
 }
-constexpr float kGsLog2e = -1.4426950408889634f;
 
 // 2 NP consecutive channels as loaded, and as pairs of fp32.
 template <typename T_, int NP>
@@ -198,7 +203,6 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : OUT ? 6 : 8)
   gs_load_f32<NP>(p.bias != nullptr ? p.bias + it.c : nullptr, bias);
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    bias[k] = mul_f32x2(bias[k], both(kGsLog2e));
     A[k] = one;
     h[k] = zero;
   }
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : OUT ? 6 : 8)
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
           float2 a, na;
-          gs_gate(fma2(gr[j].get(k), both(kGsLog2e), bias[k]), &a, &na);
+          gs_gate(gs_arg(gr[j].get(k), bias[k]), &a, &na);
           h[k] = fma2(a, h[k], mul_f32x2(na, xr[j].get(k)));
           if (!OUT) A[k] = mul_f32x2(A[k], a);
         }
@@ -270,7 +274,6 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : 8) gated_adj
   gs_load_f32<NP>(p.bias != nullptr ? p.bias + it.c : nullptr, bias);
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
-    bias[k] = mul_f32x2(bias[k], both(kGsLog2e));
     A[k] = both(1.f);
     m[k] = both(0.f);
   }
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : 8) gated_adj
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
           float2 e;
-          const float2 a = gs_keep(fma2(gr[j].get(k), both(kGsLog2e), bias[k]), &e);
+          const float2 a = gs_keep(gs_arg(gr[j].get(k), bias[k]), &e);
           m[k] = mul_f32x2(a, add2(dr[j].get(k), m[k]));
           A[k] = mul_f32x2(A[k], a);
         }
@@ -372,7 +375,6 @@ __global__ void __launch_bounds__(kGsBwdThreads, 2) gated_scan_bwd_kernel(const 
   const int s0 = it.k * p.chunk, rows = min(p.chunk, p.n - s0);
   float2 bias[1], m[1], db = both(0.f);
   gs_load_f32<1>(p.bias != nullptr ? p.bias + it.c : nullptr, bias);
-  bias[0] = mul_f32x2(bias[0], both(kGsLog2e));
   if (p.chunks > 1) gs_load_f32<1>(p.carry + (long long)it.k * p.B.d * p.D + it.bc, m);   // dh0 may be dh_last
   else gs_load_f32<1>(p.dh_last != nullptr ? p.dh_last + it.bc : nullptr, m);
   const T_* x = static_cast<const T_*>(p.x) + (long long)it.b * p.n * p.ldx + it.c;
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kGsBwdThreads, 2) gated_scan_bwd_kernel(const 
     for (int j = U - 1; j >= 0; --j)
       if (whole || j >= skip) {
         const float2 xv = xr[j].get(0);
-        gs_gate(fma2(gr[j].get(0), both(kGsLog2e), bias[0]), &a[j], &na[j]);
+        gs_gate(gs_arg(gr[j].get(0), bias[0]), &a[j], &na[j]);
         d[j] = fma2(xv, both(-1.f), h);
         h = fma2(a[j], h, mul_f32x2(na[j], xv));
       }

@@ -269,6 +269,18 @@ def test_gated_scan_extreme_gates(gate, spread, dtype):
     _scan_check(cfg, x, g, dy, kw)
 
 
+@pytest.mark.parametrize("size", [8.0, 30.0, 100.0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gated_scan_cancelling_bias(size, dtype):
+    """Large biases and gates that cancel: the gate is as good as that of the sum, whatever its parts were."""
+    cfg = M.GatedScanConfig(B=2, T=100, H=2, W=1, D=64, order=1, dtype=dtype)
+    x, g, dy, kw = _scan_inputs(cfg, 21, True)
+    kw["bias"] = (size * np.random.default_rng(22).standard_normal(cfg.D)).astype(np.float32)
+    g = (g - 2 - kw["bias"]).astype(np.float32)
+    g = mi.round_to_bf16(g) if dtype == "bf16" else g
+    _scan_check(cfg, x, g, dy, kw)
+
+
 @pytest.mark.parametrize("B", [512, 128, 64])
 def test_gated_scan_long_chunks(B):
     """Batches with so many channels that a thread walks 128, 64 or 32 rows: against the recurrence in 64 bits on the GPU,
