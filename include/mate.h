@@ -459,7 +459,9 @@ MATE_API mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, 
  *             the state before each run of rows
  * Requirements: D a multiple of 16 bytes of elements, B*T*H*W < 2^31.  ws: at least
  * mate_gated_scan_workspace_bytes(cfg) bytes (0, and ws may be null, for short sequences); calls that overlap on the GPU need workspaces of their own.
- * States and gates are fp32; the result does not change from run to run.
+ * States and gates are fp32; the result does not change from run to run.  An infinite state (from x or h0; backwards, from
+ * dy or dh_last) stays infinite and a NaN stays NaN in the rows behind it, whatever the shape; a gate of 0 (g + bias of
+ * -infinity, or below -87.3, where sigmoid is below fp32's normal numbers) makes an infinite state NaN.
  */
 typedef struct {
   int B, T, H, W, D;

@@ -125,6 +125,14 @@ __device__ __forceinline__ void gs_gate(float2 t, float2* a, float2* na) {
   na->y = t.y < 0.f ? p.y : q.y;
 }
 
+// What a run of rows leaves of the state before it: the product of its gates, in [0, 1].  Gates above 0 keep an infinite
+// state infinite, and one of 0 makes it NaN, however the rows are cut into runs: so a product of gates above 0 that is too
+// small for fp32 stays at the smallest number (of a finite state that adds at most 2^-149 |h|, what rounding such a product
+// adds, too), and 0 says that a gate was 0.  A NaN gate is in the run's H.
+__device__ __forceinline__ float gs_kept(float A, float a) {
+  return fmaxf(A * a, fminf(fminf(A, a), __uint_as_float(1u)));
+}
+
 // 2 NP consecutive channels as loaded, and as pairs of fp32.
 template <typename T_, int NP>
 struct GsRaw {
@@ -169,6 +177,35 @@ __device__ __forceinline__ void gs_load_f32(const float* p, float2 (&v)[NP]) {
 template <typename T_>
 __device__ __forceinline__ T_* gs_at(T_* p, int row, unsigned ld) {
   return p + static_cast<unsigned long long>(static_cast<unsigned>(row)) * ld;
+}
+
+// A = what a batch leaves of A, from the plain products P of its gates.  Where one came out as 0 (gates below 2^-18 on
+// average, or one of 0), the batch's gates, steps s, s + 1, .. of `order`, are multiplied again one by one.
+template <typename T_, int NP>
+__device__ __forceinline__ void gs_keep_batch(float2 (&A)[NP], float2 (&P)[NP], const GsOrder& order, unsigned s, int count,
+                                              const T_* g, unsigned ldg, const float2 (&bias)[NP]) {
+  float least = P[0].x;
+#pragma unroll
+  for (int k = 0; k < NP; ++k) least = fminf(least, fminf(P[k].x, P[k].y));
+  if (least == 0.f) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) P[k] = both(1.f);
+    GsWalk w(order, s);
+#pragma unroll 1
+    for (int j = 0; j < count; ++j) {
+      GsRaw<T_, NP> gr;
+      gr.load(gs_at(g, w.row, ldg));
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        float2 e;
+        const float2 a = gs_keep(gs_arg(gr.get(k), bias[k]), &e);
+        P[k] = make_float2(gs_kept(P[k].x, a.x), gs_kept(P[k].y, a.y));
+      }
+      w.next(order);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < NP; ++k) A[k] = make_float2(gs_kept(A[k].x, P[k].x), gs_kept(A[k].y, P[k].y));
 }
 
 // Which channels (2 NP from c on) of which chunk a thread takes.
@@ -233,6 +270,7 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : OUT ? 6 : 8)
       for (int k = 0; k < NP; ++k) reinterpret_cast<float2*>(st)[k] = h[k];
       st += p.D;
     }
+    float2 P[NP];
 #pragma unroll
     for (int j = 0; j < U; ++j)
       if (whole || i + j < rows) {
@@ -241,10 +279,11 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : OUT ? 6 : 8)
           float2 a, na;
           gs_gate(gs_arg(gr[j].get(k), bias[k]), &a, &na);
           h[k] = fma2(a, h[k], mul_f32x2(na, xr[j].get(k)));
-          if (!OUT) A[k] = mul_f32x2(A[k], a);
+          if (!OUT) P[k] = j == 0 ? a : mul_f32x2(P[k], a);
         }
         if (OUT) gs_store<T_, NP>(gs_at(y, row[j], p.ldy), h);
       }
+    if (!OUT) gs_keep_batch<T_, NP>(A, P, p.order, s0 + i, whole ? U : rows - i, g, p.ldg, bias);
   };
   int i = 0;
   for (; i + U <= rows; i += U) batch(i, std::true_type{});
@@ -291,6 +330,7 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : 8) gated_adj
         gr[j].load(gs_at(g, row[j], p.ldg));
         dr[j].load(gs_at(dy, row[j], p.lddy));
       }
+    float2 P[NP];
 #pragma unroll
     for (int j = 0; j < U; ++j)
       if (whole || i + j < rows)
@@ -299,8 +339,9 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : 8) gated_adj
           float2 e;
           const float2 a = gs_keep(gs_arg(gr[j].get(k), bias[k]), &e);
           m[k] = mul_f32x2(a, add2(dr[j].get(k), m[k]));
-          A[k] = mul_f32x2(A[k], a);
+          P[k] = j == 0 ? a : mul_f32x2(P[k], a);
         }
+    gs_keep_batch<T_, NP>(A, P, p.back, p.n - s0 - rows + i, whole ? U : rows - i, g, p.ldg, bias);
   };
   int i = 0;
   for (; i + U <= rows; i += U) batch(i, std::true_type{});
@@ -331,13 +372,13 @@ __global__ void __launch_bounds__(CH * SEG)
 #pragma unroll
     for (int j = 0; j < kGsCarryHeld; ++j) {
       H = fmaf(v[j].x, H, v[j].y);
-      A *= v[j].x;
+      A = gs_kept(A, v[j].x);
     }
 #pragma unroll 8
     for (int k = k0 + kGsCarryHeld; k < k1; ++k) {
       const float2 u = pair[at(k)];
       H = fmaf(u.x, H, u.y);
-      A *= u.x;
+      A = gs_kept(A, u.x);
     }
   }
   s[seg][lc] = make_float2(A, H);

@@ -341,6 +341,108 @@ def test_gated_scan_infinite_gates():
     np.testing.assert_array_equal(y[:, 50:100], np.repeat(x[:, 50:51], 50, 1).astype(np.float64))
 
 
+def _classes(t):
+    """0: finite, 1: inf, -1: -inf, 2: NaN."""
+    a = _np(t) if isinstance(t, torch.Tensor) else t
+    return np.where(np.isnan(a), 2, np.where(np.isinf(a), np.sign(a), 0)).astype(int)
+
+
+def _same_classes(got, ref, bound, dtype, what):
+    """Infinities and NaN as the recurrence gives them, and the finite values within their bounds."""
+    np.testing.assert_array_equal(_classes(got), _classes(ref), err_msg=what)
+    ok = np.isfinite(ref)
+    _close(_np(got)[ok], ref[ok], np.broadcast_to(bound, ref.shape)[ok], dtype, what)
+
+
+def _infinite_inputs(cfg, seed):
+    """Gates whose products leave fp32's range in a chunk (column 1 of 4), in eight rows (2), in two (3), or not at all."""
+    x, g, dy, kw = _scan_inputs(cfg, seed, True, gate=0.0)
+    g += np.array([2.0, -9.0, -20.0, -60.0], np.float32)[np.arange(cfg.D) % 4]
+    g = mi.round_to_bf16(g) if cfg.dtype == "bf16" else g
+    return x, g, dy, kw
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("order,reverse", [(0, False), (2, True)])
+def test_gated_scan_infinite_states(order, reverse, dtype):
+    """An infinite state stays infinite and a NaN stays NaN behind the row that brings it, wherever chunks begin: from x,
+    from h0, from the gradients dy and dh_last; opposite infinities meet in a NaN."""
+    cfg = M.GatedScanConfig(B=2, T=50, H=7, W=2, D=32, order=order, reverse=reverse, dtype=dtype)
+    x, g, dy, kw = _infinite_inputs(cfg, 23)
+    row = OP.scan_rows(cfg)
+    plain = [a.copy() for a in (x, dy)]
+    x[0, row[50], 0:8], x[0, row[333], 4:12], x[1, row[699], :] = np.inf, -np.inf, -np.inf
+    x[1, row[100], 8:12] = np.nan
+    kw["h0"][1, 12:24] = -np.inf
+    kw["h0"][0, 20:24] = np.nan
+    ref = OP.gated_scan(x, g, cfg, kw["bias"], kw["h0"])
+    d = {k: _dev(v) for k, v in kw.items()}
+    y, hl = M.gated_scan(_dev(x, dtype), _dev(g, dtype), cfg, bias=d["bias"], h0=d["h0"])
+    _same_classes(y, *ref["y"], dtype, "y")
+    _same_classes(hl, *ref["h_last"], "f32", "h_last")
+    assert {-1, 0, 1, 2} == set(_classes(y).ravel())
+    # the adjoint state runs back from the gradients
+    x, dy = plain
+    _, _, _, kw = _infinite_inputs(cfg, 23)
+    dy[0, row[600], 0:8], dy[0, row[30], 4:12], dy[1, row[350], 8:12] = np.inf, -np.inf, np.nan
+    kw["dh_last"][1, 12:24] = -np.inf
+    ref = OP.gated_scan(x, g, cfg, kw["bias"], kw["h0"], dy, kw["dh_last"])
+    d = {k: _dev(v) for k, v in kw.items()}
+    xd, gd, states = _dev(x, dtype), _dev(g, dtype), M.gated_scan_states(cfg)
+    M.gated_scan(xd, gd, cfg, bias=d["bias"], h0=d["h0"], states=states)
+    gr = M.gated_scan_backward(xd, gd, states, _dev(dy, dtype), cfg, bias=d["bias"], dh_last=d["dh_last"])
+    # dg = l (h - x) a (1 - a): where h and x agree to the rounding of an fp32 h (a repeated bf16 x behind a gate of e^-60),
+    # the difference may come out as 0 or with either sign, and an infinite l times it as NaN or either infinity
+    h, err = (v[:, row] for v in ref["y"])
+    before, eb = np.concatenate([kw["h0"][:, None], h[:, :-1]], axis=1), np.concatenate([0 * err[:, :1], err[:, :-1]], axis=1)
+    free = np.zeros(h.shape, bool)
+    free[:, row] = np.abs(before - x[:, row]) <= eb + OP.EPS32 * (np.abs(before) + np.abs(x[:, row]))
+    free &= ~np.isfinite(ref["dg"][0])
+    assert free.mean() < 0.01 and not np.isfinite(_np(gr["dg"])[free]).any()
+    gr["dg"][torch.as_tensor(free).cuda()] = 0
+    ref["dg"][0][free], ref["dg"][1][free] = 0, 0
+    for k, v in gr.items():
+        _same_classes(v, *ref[k], dtype if k in ("dx", "dg") else "f32", k)
+    assert {-1, 0, 1, 2} <= set(_classes(gr["dx"]).ravel()) | set(_classes(gr["dh0"]).ravel())
+
+
+@pytest.mark.parametrize("at", [3, 150, 700 - 9])
+def test_gated_scan_infinite_state_meets_a_zero_gate(at):
+    """0 times infinity: a gate of -inf makes an infinite state NaN from its row on, and starts a finite one afresh."""
+    cfg = M.GatedScanConfig(B=1, T=700, H=1, W=1, D=16, dtype="f32")
+    x, g, _, kw = _infinite_inputs(cfg, 24)
+    kw["h0"][0, :8] = np.inf
+    g[:, at] = -np.inf
+    ref = OP.gated_scan(x, np.maximum(g, -700), cfg, kw["bias"], kw["h0"])["y"]
+    y, _ = M.gated_scan(_dev(x), _dev(g), cfg, bias=_dev(kw["bias"]), h0=_dev(kw["h0"]))
+    want = np.zeros((1, 700, 16), int)
+    want[:, :at, :8], want[:, at:, :8] = 1, 2
+    np.testing.assert_array_equal(_classes(y), want)
+    _close(y[..., 8:], ref[0][..., 8:], ref[1][..., 8:], "f32", "y")
+    np.testing.assert_array_equal(_np(y)[:, at, 8:], x[:, at, 8:])
+
+
+def test_gated_scan_infinite_states_whatever_the_chunks():
+    """The same rows alone, in a batch that walks 128 rows at a time, in parts and token by token."""
+    cfg = M.GatedScanConfig(B=1, T=300, H=1, W=1, D=1024)
+    x, g, _, kw = _infinite_inputs(cfg, 25)
+    x[0, 17, :500], x[0, 200, 400:900] = np.inf, -np.inf
+    ref = OP.gated_scan(x, g, cfg, kw["bias"], kw["h0"])
+    xd, gd, b, h0 = _dev(x, "bf16"), _dev(g, "bf16"), _dev(kw["bias"]), _dev(kw["h0"])
+    y, _ = M.gated_scan(xd, gd, cfg, bias=b, h0=h0)
+    _same_classes(y, *ref["y"], "bf16", "alone")
+    many = lambda t: t.expand(512, *t.shape[1:]).contiguous()
+    yb, _ = M.gated_scan(many(xd), many(gd), dataclasses.replace(cfg, B=512), bias=b, h0=many(h0))
+    assert torch.equal(yb.view(torch.int16), yb[:1].view(torch.int16).expand_as(yb))
+    _same_classes(yb[:1], *ref["y"], "bf16", "batch")
+    h, parts = h0, []
+    cuts = [0, 100, *range(195, 206), 300]
+    for lo, hi in zip(cuts, cuts[1:]):
+        yp, h = M.gated_scan(xd[:, lo:hi].contiguous(), gd[:, lo:hi].contiguous(), dataclasses.replace(cfg, T=hi - lo), bias=b, h0=h)
+        parts.append(yp)
+    _same_classes(torch.cat(parts, dim=1), *ref["y"], "bf16", "parts")
+
+
 @pytest.mark.parametrize("order,reverse", [(0, False), (0, True)])
 def test_gated_scan_in_parts(order, reverse):
     """A video in parts, the last token by token: h_last handed on as h0 gives the whole run's rows and state."""
