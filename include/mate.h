@@ -408,7 +408,9 @@ MATE_API mate_status mate_dit_block_forward(const void* X, const float* c, int d
  * Tables: [T][rt/2], [H][rh/2], [W][rw/2] pairs (cos, sin) of floats, as mate_rope_table writes them (any table
  * of that layout serves; a later part of a video passes tables that start at its first frame).
  * Requirements: rt, rh, rw even, rt + rh + rw <= tp, tp <= 256, tp a multiple of 16 bytes of elements, hq and
- * hk at least 1, eps > 0, B*T*H*W < 2^31.  fp32 arithmetic, one rounding at the end.
+ * hk at least 1, eps > 0, B*T*H*W < 2^31; rows start on 16 bytes, wq, wk and the tables on 8.  fp32 arithmetic
+ * (squares included: a channel of 2^63 or more makes its head's mean infinite and its other channels 0), one rounding
+ * at the end.
  */
 typedef struct {
   int B, T, H, W;
@@ -458,7 +460,9 @@ MATE_API mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, 
  *   states    (null: not wanted) for the backward pass: mate_gated_scan_states_bytes(cfg) bytes, overwritten with
  *             the state before each run of rows
  * Requirements: D a multiple of 16 bytes of elements, B*T*H*W < 2^31.  ws: at least
- * mate_gated_scan_workspace_bytes(cfg) bytes (0, and ws may be null, for short sequences); calls that overlap on the GPU need workspaces of their own.
+ * mate_gated_scan_workspace_bytes(cfg) bytes (0, and ws may be null, for short sequences); calls that overlap on the
+ * GPU need workspaces of their own.  Rows start on 16 bytes; bias, h0, h_last and states, and the backward pass'
+ * dh_last, dh0 and dbias, on 8.
  * States and gates are fp32; the result does not change from run to run.  An infinite state (from x or h0; backwards, from
  * dy or dh_last) stays infinite and a NaN stays NaN in the rows behind it, whatever the shape; a gate of 0 (g + bias of
  * -infinity, or below -87.3, where sigmoid is below fp32's normal numbers) makes an infinite state NaN.
@@ -504,6 +508,7 @@ MATE_API mate_status mate_gated_scan_backward(const void* x, long long ldx, cons
  * mate_project_int8: C[m, n] = (sum_k A[m, k] W[n, k]) a_scale[m] w_scale[n] + bias[n], the sum exact in 32 bits,
  * the rest in fp32, rounded once to out_dtype.  A [M, K] and Wt [N, K] int8 (row strides lda, ldw, multiples of 16,
  * any K < 131072), a_scale [M], w_scale [N], bias [N] (null: none) float, C [M, N] (row stride ldc >= N elements).
+ * A and Wt start on 16 bytes, w_scale, bias and C on 8 (rows of C that all start on 16 are stored faster).
  * M = 0 does nothing; M, N and mate_quantize_rows' K are at most 2^31 - 2^14.
  */
 MATE_API mate_status mate_quantize_rows(const void* x, long long ldx, long long M, int K, mate_dtype dtype, void* q,

@@ -221,7 +221,7 @@ struct Int8GemmParams {
   const float* bias;   // or null
   void* C;
   long long ldc;
-  int vec;             // rows of C start on 16 bytes: TMA stores
+  int vec;             // every row of C starts on 16 bytes: TMA stores
 };
 
 struct Int8Maps {

@@ -4,6 +4,7 @@
 
 namespace {
 
+// What the kernels read and write in pairs of floats or one by one; rows of tensors start on 16 bytes (aligned16).
 bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 // ------------------------------------------------------------------------------ q/k norm with rotation
@@ -35,7 +36,7 @@ mate_status fill_qk(const mate_qk_config* c, const void* x, long long ldx, const
                     const float* tt, const float* th, const float* tw, QkParams* p) {
   const long long width = ((long long)c->hq + c->hk + c->hv) * c->tp;
   const int es = c->dtype == MATE_BF16 ? 2 : 4;
-  if (x == nullptr || !aligned16(x) || !aligned16(wq) || !aligned16(wk) || !row_stride_ok(ldx, width, es))
+  if (x == nullptr || !aligned16(x) || !aligned8(wq) || !aligned8(wk) || !row_stride_ok(ldx, width, es))
     return MATE_ERR_ARG;
   if ((c->rt > 0 && tt == nullptr) || (c->rh > 0 && th == nullptr) || (c->rw > 0 && tw == nullptr) || !aligned8(tt) ||
       !aligned8(th) || !aligned8(tw))
@@ -238,7 +239,7 @@ GsOrder gated_order(const mate_gated_scan_config* c, int reverse) {
 mate_status fill_gated(const mate_gated_scan_config* c, const void* x, long long ldx, const void* g, long long ldg,
                        const float* bias, GatedScanParams* p) {
   const int es = c->dtype == MATE_BF16 ? 2 : 4;
-  if (x == nullptr || g == nullptr || !aligned16(x) || !aligned16(g) || !aligned16(bias) ||
+  if (x == nullptr || g == nullptr || !aligned16(x) || !aligned16(g) || !aligned8(bias) ||
       !row_stride_ok(ldx, c->D, es) || !row_stride_ok(ldg, c->D, es))
     return MATE_ERR_ARG;
   p->x = x;
@@ -320,8 +321,8 @@ mate_status mate_gated_scan(const void* x, long long ldx, const void* g, long lo
   MATE_TRY(fill_gated(cfg, x, ldx, g, ldg, bias, &p));
   const bool bf = cfg->dtype == MATE_BF16;
   const size_t need = mate_gated_scan_workspace_bytes(cfg);
-  if (y == nullptr || y == x || y == g || !aligned16(y) || !row_stride_ok(ldy, cfg->D, bf ? 2 : 4) || !aligned16(h0) ||
-      !aligned16(h_last) || !aligned16(states) || !aligned16(ws) || (ws == nullptr && need > 0))
+  if (y == nullptr || y == x || y == g || !aligned16(y) || !row_stride_ok(ldy, cfg->D, bf ? 2 : 4) || !aligned8(h0) ||
+      !aligned8(h_last) || !aligned8(states) || !aligned16(ws) || (ws == nullptr && need > 0))
     return MATE_ERR_ARG;
   if (ws_bytes < need) return MATE_ERR_WORKSPACE;
   const GatedScanScratch s = carve_gated(cfg, ws, false);
@@ -364,9 +365,9 @@ mate_status mate_gated_scan_backward(const void* x, long long ldx, const void* g
   MATE_TRY(fill_gated(cfg, x, ldx, g, ldg, bias, &p));
   const bool bf = cfg->dtype == MATE_BF16;
   const int es = bf ? 2 : 4;
-  if (states == nullptr || dy == nullptr || dx == nullptr || dg == nullptr || ws == nullptr || !aligned16(states) ||
-      !aligned16(dy) || !aligned16(dx) || !aligned16(dg) || !aligned16(dh_last) || !aligned16(dbias) ||
-      !aligned16(dh0) || !aligned16(ws) || !row_stride_ok(lddy, cfg->D, es) || !row_stride_ok(lddx, cfg->D, es) ||
+  if (states == nullptr || dy == nullptr || dx == nullptr || dg == nullptr || ws == nullptr || !aligned8(states) ||
+      !aligned16(dy) || !aligned16(dx) || !aligned16(dg) || !aligned8(dh_last) || !aligned8(dbias) ||
+      !aligned8(dh0) || !aligned16(ws) || !row_stride_ok(lddy, cfg->D, es) || !row_stride_ok(lddx, cfg->D, es) ||
       !row_stride_ok(lddg, cfg->D, es))
     return MATE_ERR_ARG;
   for (const void* in : {x, g, dy})
@@ -506,7 +507,7 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   if (A == nullptr || a_scale == nullptr || Wt == nullptr || w_scale == nullptr || C == nullptr || M < 0 || K <= 0 ||
       N <= 0 || M > kI8MaxSize || N > kI8MaxSize)
     return MATE_ERR_ARG;
-  if (!aligned16(A) || !aligned16(Wt) || !aligned16(C) || !aligned16(w_scale) || !aligned16(bias) ||
+  if (!aligned16(A) || !aligned16(Wt) || !aligned8(C) || !aligned8(w_scale) || !aligned8(bias) ||
       (reinterpret_cast<uintptr_t>(a_scale) & 3u) || !row_stride_ok(lda, K, 1) || !row_stride_ok(ldw, K, 1) || ldc < N ||
       ldc >= (1LL << 31))
     return MATE_ERR_ARG;
@@ -553,7 +554,7 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   p.bias = bias;
   p.C = C;
   p.ldc = ldc;
-  p.vec = ldc * (out_dtype == MATE_BF16 ? 2 : 4) % 16 == 0;
+  p.vec = aligned16(C) && ldc * (out_dtype == MATE_BF16 ? 2 : 4) % 16 == 0;
   // Keep W in shared memory where that is the shorter way: its tiles take 1 / kI8KeepGain of the others' time, but the
   // pairs share out whole column tiles.  65536 x 1024 x 4368 (64 tiles a pair against 63): 232 us against 256;
   // 16384 x 1024 x 4096 (16 against 14): 65 against 59.

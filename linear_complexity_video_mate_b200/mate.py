@@ -400,6 +400,16 @@ def _flat(t: Optional[torch.Tensor], dtype: torch.dtype, numel: int, index: int,
     return t.data_ptr()
 
 
+def _check(status: int, where: str, **tensors: Optional[torch.Tensor]) -> None:
+    """check, naming the tensors whose start or rows the library may have refused."""
+    if status == _lib.MATE_ERR_ARG:
+        for name, t in tensors.items():
+            step = t.stride(-2) * t.element_size() if t is not None and t.dim() > 1 else 0
+            if t is not None and (t.data_ptr() % 16 or step % 16):
+                where += f", {name}: starts {t.data_ptr() % 16} bytes behind a multiple of 16, rows {step} bytes apart"
+    _lib.check(status, where)
+
+
 def _workspace(ws: Optional[torch.Tensor], nbytes: int, like: torch.Tensor) -> Optional[torch.Tensor]:
     """The caller's workspace (uint8, checked), else a new one of the current stream; None where none is needed."""
     if ws is None:
@@ -508,7 +518,8 @@ def qk_norm_rope(qkv: torch.Tensor, wq: Optional[torch.Tensor], wk: Optional[tor
         st = _lib.load().mate_qk_norm_rope(
             qkv.data_ptr(), ldi, _flat(wq, torch.float32, cfg.tp, index, "wq"),
             _flat(wk, torch.float32, cfg.tp, index, "wk"), *tabs, out.data_ptr(), ldo, cfg.ref, _raw_stream(index))
-    _lib.check(st, "mate_qk_norm_rope")
+    if st:
+        _check(st, "mate_qk_norm_rope", qkv=qkv, wq=wq, wk=wk, out=out)
     return out
 
 
@@ -534,7 +545,8 @@ def qk_norm_rope_backward(qkv: torch.Tensor, wq: Optional[torch.Tensor], wk: Opt
             qkv.data_ptr(), ldi, _flat(wq, torch.float32, cfg.tp, index, "wq"),
             _flat(wk, torch.float32, cfg.tp, index, "wk"), *tabs, dout.data_ptr(), ldg, dqkv.data_ptr(), ldd,
             dwq.data_ptr(), dwk.data_ptr(), cfg.ref, ws.data_ptr(), ws.numel(), _raw_stream(index))
-    _lib.check(st, "mate_qk_norm_rope_backward")
+    if st:
+        _check(st, "mate_qk_norm_rope_backward", qkv=qkv, wq=wq, wk=wk, dout=dout, dqkv=dqkv)
     return dict(dqkv=dqkv, dwq=dwq, dwk=dwk)
 
 
@@ -603,7 +615,8 @@ def gated_scan(x: torch.Tensor, g: torch.Tensor, cfg: GatedScanConfig, bias: Opt
             _flat(h0, f32, cfg.B * D, index, "h0"), y.data_ptr(), ldy, _flat(h_last, f32, cfg.B * D, index, "h_last"),
             None if states is None else _flat(states, f32, cfg.states_numel, index, "states"), cfg.ref,
             None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _raw_stream(index))
-    _lib.check(st, "mate_gated_scan")
+    if st:
+        _check(st, "mate_gated_scan", x=x, g=g, bias=bias, h0=h0, y=y, h_last=h_last, states=states)
     return y, h_last
 
 
@@ -635,7 +648,8 @@ def gated_scan_backward(x: torch.Tensor, g: torch.Tensor, states: torch.Tensor, 
             _flat(dh_last, f32, cfg.B * D, index, "dh_last"), dx.data_ptr(), _rows(dx, dt, rows, D, index, "dx"),
             dg.data_ptr(), _rows(dg, dt, rows, D, index, "dg"), None if dbias is None else dbias.data_ptr(),
             grads["dh0"].data_ptr(), cfg.ref, ws.data_ptr(), ws.numel(), _raw_stream(index))
-    _lib.check(st, "mate_gated_scan_backward")
+    if st:
+        _check(st, "mate_gated_scan_backward", x=x, g=g, states=states, dy=dy, bias=bias, dh_last=dh_last, dx=dx, dg=dg)
     return grads
 
 
@@ -664,7 +678,8 @@ def quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None, scale: Opti
             scale = torch.empty(M, dtype=torch.float32, device=x.device)
         st = _lib.load().mate_quantize_rows(x.data_ptr(), ldx, M, K, code, q.data_ptr(), ldq,
                                             _flat(scale, torch.float32, M, index, "scale"), _raw_stream(index)) if M else 0
-    _lib.check(st, "mate_quantize_rows")
+    if st:
+        _check(st, "mate_quantize_rows", x=x, q=q, scale=scale)
     return q, scale
 
 
@@ -689,7 +704,8 @@ def project_int8(A: torch.Tensor, a_scale: torch.Tensor, Wt: torch.Tensor, w_sca
             A.data_ptr(), lda, _flat(a_scale, f32, M, index, "a_scale"), M, K, Wt.data_ptr(), ldw,
             _flat(w_scale, f32, N, index, "w_scale"), N, _flat(bias, f32, N, index, "bias"), out.data_ptr(), ldc, code,
             _raw_stream(index)) if M else 0
-    _lib.check(st, "mate_project_int8")
+    if st:
+        _check(st, "mate_project_int8", A=A, a_scale=a_scale, Wt=Wt, w_scale=w_scale, bias=bias, out=out)
     return out
 
 

@@ -683,6 +683,68 @@ def test_project_int8_empty_and_nan_rows():
     assert torch.isnan(out[1]).all() and (out[2] == 0).all() and torch.isfinite(out[[0, 3]]).all()
 
 
+# ------------------------------------------------------------------------------------------------ alignment
+def _at8(t):
+    """The same values in a tensor that starts 8 bytes behind a multiple of 16."""
+    n = 8 // t.element_size()
+    big = torch.zeros(t.numel() + n, dtype=t.dtype, device=t.device)
+    big[n:] = t.flatten()
+    return big[n:].view(t.shape)
+
+
+def test_vectors_on_8_bytes():
+    """Weights, biases, scales and states that are slices of larger tensors: the same bits as on 16 bytes."""
+    qk = QK[2]
+    rng, qkv, (wq, wk), tabs, _ = _qk_inputs(qk, 26)
+    x, d, wq, wk = _dev(qkv, "bf16"), _dev(_host(rng, qkv.shape, "bf16"), "bf16"), _dev(wq), _dev(wk)
+    tabs8 = [_at8(t) for t in tabs]
+    assert torch.equal(M.qk_norm_rope(x, wq, wk, tabs, qk), M.qk_norm_rope(x, _at8(wq), _at8(wk), tabs8, qk))
+    want, got = M.qk_norm_rope_backward(x, wq, wk, tabs, d, qk), M.qk_norm_rope_backward(x, _at8(wq), _at8(wk), tabs8, d, qk)
+    assert all(torch.equal(want[k], got[k]) for k in want)
+    for cfg in (SCAN[2], SCAN[7], SCAN[11]):
+        x, g, dy, kw = _scan_inputs(cfg, 27, True)
+        x, g, dy, kw = _dev(x, cfg.dtype), _dev(g, cfg.dtype), _dev(dy, cfg.dtype), {k: _dev(v) for k, v in kw.items()}
+        kw8 = {k: _at8(v) for k, v in kw.items()}
+        res = []
+        for w, at in ((kw, lambda t: t), (kw8, _at8)):
+            st, hl = at(M.gated_scan_states(cfg)), at(torch.zeros((cfg.B, cfg.D), device="cuda"))
+            y, _ = M.gated_scan(x, g, cfg, bias=w["bias"], h0=w["h0"], h_last=hl, states=st)
+            res.append((y, hl, *M.gated_scan_backward(x, g, st, dy, cfg, bias=w["bias"], dh_last=w["dh_last"]).values()))
+        assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("M_,K,N", [(2, 256, 96), (300, 1024, 1000), (20000, 1000, 600)])
+def test_project_int8_on_8_bytes(M_, K, N, dtype):
+    """Scales and biases of some of the channels, and an output whose rows start 8 bytes behind a multiple of 16."""
+    gen = torch.Generator(device="cuda").manual_seed(28)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    A, W = (torch.randint(-127, 128, (r, (K + 15) // 16 * 16), generator=gen, device="cuda", dtype=torch.int8)[:, :K]
+            for r in (M_, N))
+    sa, sw, b = (torch.rand(n, generator=gen, device="cuda") for n in (M_, N, N))
+    want = M.project_int8(A, sa, W, sw, bias=b, out_dtype=dt)
+    c0 = 8 // want.element_size()
+    big = torch.full((M_, N + (-N % 8) + 16), float("nan"), dtype=dt, device="cuda")
+    M.project_int8(A, sa, W, _at8(sw), bias=_at8(b), out=big[:, c0:c0 + N])
+    assert torch.equal(big[:, c0:c0 + N], want)
+    assert torch.isnan(big[:, :c0]).all() and torch.isnan(big[:, c0 + N:]).all()
+
+
+def test_refusals_name_the_tensor():
+    """What starts at an odd place is refused by name."""
+    A, s = torch.ones((4, 32), dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
+    with pytest.raises(_lib.MateError, match="w_scale: starts 4 bytes"):
+        M.project_int8(A, s[:4], A, s[1:5])
+    with pytest.raises(_lib.MateError, match="out: starts 2 bytes"):
+        M.project_int8(A, s[:4], A, s[:4], out=torch.zeros((4, 8), dtype=torch.bfloat16, device="cuda")[:, 1:5])
+    with pytest.raises(_lib.MateError, match="x: .* rows 200 bytes apart"):
+        M.quantize_rows(torch.zeros((4, 100), dtype=torch.bfloat16, device="cuda"))
+    cfg = M.GatedScanConfig(B=1, T=4, H=1, W=1, D=32, dtype="f32")
+    x = torch.zeros((4, 32), device="cuda")
+    with pytest.raises(_lib.MateError, match="h0: starts 4 bytes"):
+        M.gated_scan(x, x, cfg, h0=s[1:33])
+
+
 # ---------------------------------------------------------------------------- graphs, streams, the run together
 def _together_ref(cfg, qk, gs, w):
     """The mixing block in fp64, with the rounding of every stored tensor."""
