@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(128) gemm_int8_few_kernel(const int8_t* __rest
 // An MMA takes 128 cycles (256 x 256 x 32) and reads 8 KB of each CTA's shared memory meanwhile, half of what that
 // memory gives; the loads of a stage write as much again, and the epilogue stages its output there too.  So shared
 // memory is what bounds the product at short K, and both sides are kept low:
-//   KEEP: for K <= kI8KeepK a CTA's half of a column tile of W stays in shared memory while the pair walks down the
+//   KEEP: for K <= kI8KeepK (fp32 output: kI8KeepKF32) a CTA's half of a column tile of W stays in shared memory while the pair walks down the
 //   rows, so that only A streams;
 //   the epilogue writes a slice of the output to shared memory once and a TMA store takes it from there.
 // 262,144 x 1024 x 4368: 0.87 ms, 2.7 Poperations/s, tensor pipe 67% active (without the two: 1.08 ms, 53%);
@@ -229,7 +229,7 @@ struct Int8Maps {
 };
 
 constexpr int kI8BK = 128;                               // bytes of K per stage
-constexpr int kI8KeepK = 1024;
+constexpr int kI8KeepK = 1024, kI8KeepKF32 = 768;
 constexpr int kI8TileStart = 32;   // what a tile costs beside its columns, in columns (small problems)
 constexpr int kI8EpiWarps = 8;
 constexpr int kI8Threads = (2 + kI8EpiWarps) * 32;

@@ -556,17 +556,19 @@ mate_status mate_project_int8(const void* A, long long lda, const float* a_scale
   p.ldc = ldc;
   p.vec = aligned16(C) && ldc * (out_dtype == MATE_BF16 ? 2 : 4) % 16 == 0;
   // Keep W in shared memory where that is the shorter way: its tiles take 1 / kI8KeepGain of the others' time, but the
-  // pairs share out whole column tiles.  65536 x 1024 x 4368 (64 tiles a pair against 63): 232 us against 256;
-  // 16384 x 1024 x 4096 (16 against 14): 65 against 59.
+  // pairs share out whole column tiles.  65536 x 1024 x 4368 (64 tiles a pair against 63): 250 us against 263;
+  // 16384 x 1024 x 4096 (16 against 14): 68 against 60.  fp32 output is staged in twice the space, and stops gaining where
+  // W leaves fewer than five stages for A.  65536 rows, fp32: K = 512, N = 4368 213 us kept, 220 streamed; K = 768, N = 2048
+  // 119 and 119; K = 896, N = 2048 145 and 133; K = 1024, N = 4368 346 and 309.
   constexpr double kI8KeepGain = 1.1;
   const int mblocks = ceil_div(M, 256);
   int pairs = std::min(p.num_tiles, pairs_all);
   p.slots = std::min(p.num_n_tiles, pairs_all);
   p.groups = std::min(pairs_all / p.slots, mblocks);
   const long long kept_tiles = (long long)ceil_div(p.num_n_tiles, p.slots) * ceil_div(mblocks, p.groups);
-  const bool keep = K <= kI8KeepK && p.bn == 256 && kept_tiles < kI8KeepGain * ceil_div(p.num_tiles, pairs);
-  if (keep) pairs = p.slots * p.groups;
   const int es = out_dtype == MATE_BF16 ? 2 : 4;
+  const bool keep = K <= (es == 2 ? kI8KeepK : kI8KeepKF32) && p.bn == 256 && kept_tiles < kI8KeepGain * ceil_div(p.num_tiles, pairs);
+  if (keep) pairs = p.slots * p.groups;
   const uint32_t sb = int8_stage_bytes(p.bn, keep);
   const uint32_t fixed = 1024 + int8_kept_bytes(p.bn, K, keep) + int8_out_bytes(es) + kI8Behind;
   p.stages = std::min<int>(8, static_cast<int>((kSmemLimit - fixed) / sb));

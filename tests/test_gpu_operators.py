@@ -590,6 +590,19 @@ def test_quantize_bf16_midpoints(few):
     assert exact.any() and (few or len(x) >= 6 * torch.cuda.get_device_properties(0).multi_processor_count)
 
 
+@pytest.mark.parametrize("K", [769, 1024])
+def test_project_int8_f32_streams_long_rows(K):
+    """fp32 output beyond 768 bytes of K: the weights are streamed where bf16 output keeps them, to the same sums."""
+    assert _int8_rule(20000, K, 600, "f32") == (256, False) and _int8_rule(20000, K, 600, "bf16") == (256, True)
+    gen = torch.Generator(device="cuda").manual_seed(K)
+    A, W = (torch.randint(-128, 128, (r, (K + 15) // 16 * 16), generator=gen, device="cuda", dtype=torch.int8)[:, :K]
+            for r in (20000, 600))
+    one = torch.ones(20000, device="cuda")
+    out = M.project_int8(A, one, W, one[:600], out_dtype=torch.float32)
+    assert torch.equal(out.double(), A.double() @ W.double().t())   # sums below 2^24: exact in fp32, too
+    assert torch.equal(M.project_int8(A, one, W, one[:600]), out.bfloat16())
+
+
 INT8 = [(1, 16, 1), (1, 1024, 96), (2, 2048, 1001), (5, 100, 37), (8, 4096, 4096), (9, 1040, 513), (16, 512, 264),
         (17, 256, 256), (64, 333, 2048), (129, 128, 255), (257, 144, 288), (300, 1024, 1000), (513, 2048, 520), (1000, 80, 4368),
         (2000, 1024, 300), (600, 48, 19240), (10000, 250, 600), (4000, 1025, 777), (4, 4096, 100), (3, 31, 9),
@@ -620,7 +633,7 @@ def test_project_int8(M_, K, N, dtype):
     assert M.device_status() == 0
 
 
-def _int8_rule(M_, K, N):
+def _int8_rule(M_, K, N, dtype):
     """(tile columns, whether W's column tiles are kept in shared memory) that the library's rule gives on this GPU."""
     up = lambda a, b: -(-a // b)
     pairs = torch.cuda.get_device_properties(0).multi_processor_count // 2
@@ -630,18 +643,18 @@ def _int8_rule(M_, K, N):
     nt = up(N, bn)
     slots = min(nt, pairs)
     groups = min(pairs // slots, mb)
-    return bn, K <= 1024 and bn == 256 and up(nt, slots) * up(mb, groups) < 1.1 * up(mb * nt, min(mb * nt, pairs))
+    return bn, K <= (1024 if dtype == "bf16" else 768) and bn == 256 and up(nt, slots) * up(mb, groups) < 1.1 * up(mb * nt, min(mb * nt, pairs))
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("M_,K,N", [(65536, 1024, 512),   # 7 row tiles a pair, the ring of A wraps, accumulators reused
-                                    (20000, 1000, 600),   # the last block of K and the last tiles cut
-                                    (512, 144, 37888),    # a second column tile over the first
-                                    (512, 1000, 56700)])  # a third one, cut, with more blocks of K than the ring holds
+@pytest.mark.parametrize("M_,K,N,dtype", [
+    (65536, 1024, 512, "bf16"), (65536, 768, 512, "f32"),    # 7 row tiles a pair, the ring of A wraps, accumulators reused
+    (20000, 1000, 600, "bf16"), (20000, 700, 600, "f32"),    # the last block of K and the last tiles cut
+    (512, 144, 37888, "bf16"), (512, 144, 37888, "f32"),     # a second column tile over the first
+    (512, 1000, 56700, "bf16"), (512, 760, 56700, "f32")])   # a third one, cut, with more blocks of K than the ring holds
 def test_project_int8_kept_weights(M_, K, N, dtype):
     """W kept in shared memory while a pair walks down the rows: reused accumulators and ring stages, column tiles loaded
     over earlier ones; launch after launch, since a CTA may not leave before its last arrivals are in."""
-    assert _int8_rule(M_, K, N) == (256, True)
+    assert _int8_rule(M_, K, N, dtype) == (256, True)
     gen = torch.Generator(device="cuda").manual_seed(M_ + K)
     ints = lambda r: torch.randint(-128, 128, (r, (K + 15) // 16 * 16), generator=gen, device="cuda", dtype=torch.int8)[:, :K]
     A, W = ints(M_), ints(N)
