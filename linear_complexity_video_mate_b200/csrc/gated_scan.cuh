@@ -12,8 +12,9 @@
 //   3. gated_scan_kernel<true>   the rows again from that state, y out.
 // Every x and g is read twice (the last-read rows from L2: step 3 starts where step 1 ended), five streams instead of
 // the three that cannot be avoided.  One pass with the chunks' pairs handed on between running blocks was built and
-// measured too: it moves three, but needs 60 instructions per two values instead of 48 (staging, joins, waiting) and
-// leaves the blocks in step, all waiting for the slowest: 700 us for 262,144 rows of 1024 channels.
+// measured too: it moves three, but needs as many instructions as the two row steps together (60 per two values: staging,
+// joins, waiting) and leaves the blocks in step, all waiting for the slowest: 700 us for 262,144 rows of 1024 channels,
+// where the three steps take 483.
 // A sequence of one chunk takes step 3 alone.
 #pragma once
 #include "common.cuh"
@@ -224,8 +225,9 @@ struct GsItem {
 
 // Four channels of a chunk per thread.  OUT: y from the state before the chunk (and the states every kGsState rows, the
 // last state); else the chunk's pair.  Bound by HBM with eight rows of two tensors in flight per thread: 262,144 rows of
-// 1024 bf16 channels take 185 us for the pairs (0.89 of the measured copy rate) and 255 us for y (0.96); more registers
-// for y's step (fewer blocks) cost 25%, and with guards on every row and its position the two took 228 and 299 us.
+// 1024 bf16 channels take 209 us for the pairs (0.78 of the measured copy rate; 190 before g and the bias were added first,
+// 205 before products of gates were kept above 0) and 257 us for y (0.96); more registers for y's step (fewer blocks) cost
+// 25%, and guards on every row and its position some 20%.
 template <typename T_, bool OUT>
 __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : OUT ? 6 : 8) gated_scan_kernel(const GatedScanParams p) {
   constexpr int NP = 2, U = kGsBatch;
@@ -299,8 +301,8 @@ __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : OUT ? 6 : 8)
   }
 }
 
-// The chunks' pairs of the adjoint state, m -> A m + M from the row behind a chunk to the row before it (56 us for 65,536
-// rows of 1024 bf16 channels, two streams: 0.74 of the copy rate).
+// The chunks' pairs of the adjoint state, m -> A m + M from the row behind a chunk to the row before it (60 us for 65,536
+// rows of 1024 bf16 channels, two streams: 0.68 of the copy rate).
 template <typename T_>
 __global__ void __launch_bounds__(kGsThreads, sizeof(T_) == 4 ? 4 : 8) gated_adjoint_kernel(const GatedScanParams p) {
   constexpr int NP = 2, U = kGsBatch;
@@ -403,9 +405,10 @@ __global__ void __launch_bounds__(CH * SEG)
 }
 
 // Gradients: two channels of a chunk per thread, kGsState rows at a time from the last to the first.  Their states are
-// formed again from the saved one, then the adjoint state walks back over them.  142 us for 65,536 rows of 1024 bf16
-// channels (five streams and the states: 0.75 of the copy rate), bound by the loads in flight at 128 registers: sixteen
-// rows at a time spilled (541 us), blocks of 128 threads, half a KB of a row each, took 162 us, 80 registers 164 us.
+// formed again from the saved one, then the adjoint state walks back over them.  148 us for 65,536 rows of 1024 bf16
+// channels (five streams and the states: 0.73 of the copy rate), bound by the loads in flight at 128 registers: sixteen
+// rows at a time spilled (3.8 times the time), blocks of 128 threads, half a KB of a row each, took 14% longer, 80 registers
+// 15%.
 template <typename T_>
 __global__ void __launch_bounds__(kGsBwdThreads, 2) gated_scan_bwd_kernel(const GatedScanParams p) {
   constexpr int U = kGsState;

@@ -186,12 +186,14 @@ mate_status mate_qk_norm_rope_backward(const void* qkv, long long ldi, const flo
 namespace {
 
 // Rows per chunk: long chunks carry little, but there have to be threads enough (four channels of a chunk each) to fill
-// the SMs.
+// the SMs.  The number of threads is fixed, not asked of the device: the workspace's size goes by cfg alone and has to be the
+// same wherever the call runs, and so do the results, which a chunk's border rounds.
+constexpr long long kGsFillThreads = 1024LL * 148;
 int gated_chunk(const mate_gated_scan_config* c) {
   const long long n = (long long)c->T * c->H * c->W, cols = (long long)c->B * (c->D / 4);
   if (n <= kGsOneChunk) return static_cast<int>(n);
   int r = kGsMaxChunk;
-  while (r > 16 && (n + r - 1) / r * cols < 1024LL * 148) r /= 2;
+  while (r > 16 && (n + r - 1) / r * cols < kGsFillThreads) r /= 2;
   return r;
 }
 
