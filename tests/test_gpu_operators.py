@@ -362,6 +362,7 @@ def _infinite_inputs(cfg, seed):
     return x, g, dy, kw
 
 
+@pytest.mark.filterwarnings("ignore:invalid value:RuntimeWarning")
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("order,reverse", [(0, False), (2, True)])
 def test_gated_scan_infinite_states(order, reverse, dtype):
@@ -406,6 +407,7 @@ def test_gated_scan_infinite_states(order, reverse, dtype):
     assert {-1, 0, 1, 2} <= set(_classes(gr["dx"]).ravel()) | set(_classes(gr["dh0"]).ravel())
 
 
+@pytest.mark.filterwarnings("ignore:invalid value:RuntimeWarning")
 @pytest.mark.parametrize("at", [3, 150, 700 - 9])
 def test_gated_scan_infinite_state_meets_a_zero_gate(at):
     """0 times infinity: a gate of -inf makes an infinite state NaN from its row on, and starts a finite one afresh."""
@@ -422,6 +424,7 @@ def test_gated_scan_infinite_state_meets_a_zero_gate(at):
     np.testing.assert_array_equal(_np(y)[:, at, 8:], x[:, at, 8:])
 
 
+@pytest.mark.filterwarnings("ignore:invalid value:RuntimeWarning")
 def test_gated_scan_infinite_states_whatever_the_chunks():
     """The same rows alone, in a batch that walks 128 rows at a time, in parts and token by token."""
     cfg = M.GatedScanConfig(B=1, T=300, H=1, W=1, D=1024)
@@ -871,3 +874,107 @@ def test_streams():
     for (y, h), q in got:
         assert torch.equal(y, want_y) and torch.equal(h, want_h) and torch.equal(q, want_q)
     assert M.device_status() == 0
+
+
+def _everything(seed):
+    """One call of every operator, forward and backward, that returns all outputs; and its inputs, to be changed between runs."""
+    qk, gs = QK[3], dataclasses.replace(SCAN[7], T=700, D=264)
+    rng, qkv, (wq, wk), tabs, _ = _qk_inputs(qk, seed)
+    x, g, dy, kw = _scan_inputs(gs, seed, True)
+    W, sw = M.quantize_rows(_dev(rng.standard_normal((5000, 304))))
+    io = dict(qkv=_dev(qkv, "bf16"), dz=_dev(_host(rng, qkv.shape, "bf16"), "bf16"), x=_dev(x, "bf16"), g=_dev(g, "bf16"),
+              dy=_dev(dy, "bf16"), a=_dev(rng.standard_normal((12000, 304)), "bf16"))
+    wq, wk, bias, sb = _dev(wq), _dev(wk), _dev(kw["bias"]), _dev(rng.standard_normal(5000))
+    h0, dhl = _dev(kw["h0"]), _dev(kw["dh_last"])
+
+    def run():
+        out = [M.qk_norm_rope(io["qkv"], wq, wk, tabs, qk)]
+        out += M.qk_norm_rope_backward(io["qkv"], wq, wk, tabs, io["dz"], qk).values()
+        st = M.gated_scan_states(gs)
+        out += M.gated_scan(io["x"], io["g"], gs, bias=bias, h0=h0, states=st)
+        out += M.gated_scan_backward(io["x"], io["g"], st, io["dy"], gs, bias=bias, dh_last=dhl).values()
+        q, s = M.quantize_rows(io["a"])
+        for rows, dt in ((12000, torch.bfloat16), (12000, torch.float32), (40, torch.bfloat16), (3, torch.float32)):
+            out.append(M.project_int8(q[:rows], s[:rows], W, sw, bias=sb, out_dtype=dt))
+        return out
+
+    return io, run
+
+
+def test_training_graphs_replayed_beside_each_other():
+    """Every forward and backward pass captured into two graphs that are replayed at the same time on two streams, with new
+    inputs, beside eager calls on a third: the bits of eager calls alone."""
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    graphs, ios, runs, outs = [], [], [], []
+    for k, s in enumerate(sides):
+        io, run = _everything(30 + k)
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            run()
+        s.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs.append(run())
+        graphs.append(graph), ios.append(io), runs.append(run)
+    for rep in range(3):
+        for io in ios:
+            for t in io.values():
+                t.copy_(t.flip(0) * (0.5 + rep))
+        want = [run() for run in runs]
+        torch.cuda.synchronize()
+        for s, graph in zip(sides, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        beside = runs[0]()
+        torch.cuda.synchronize()
+        for w, o in zip(want, outs):
+            assert len(w) == len(o) and all(torch.equal(a, b) for a, b in zip(w, o))
+        assert all(torch.equal(a, b) for a, b in zip(want[0], beside))
+    assert M.device_status() == 0
+
+
+def test_offsets_past_32_bits():
+    """Rows a million elements apart, so that the last ones lie more than 2^32 elements in: the bits of packed rows."""
+    ld, rows = (1 << 20) + 32, 4200
+    assert ld * rows > 1 << 32
+    gen = torch.Generator(device="cuda").manual_seed(33)
+    rnd = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()
+    big = torch.empty((rows, ld), dtype=torch.bfloat16, device="cuda")
+
+    def far(t, at):
+        view = big[:, at:at + t.shape[1]]
+        view.copy_(t)
+        return view
+
+    none = torch.zeros((rows, 1), dtype=torch.bfloat16, device="cuda")
+    qk = M.QkConfig(B=2, T=21, H=10, W=10, hq=2, hk=1, hv=1, tp=64, rt=16, rh=24, rw=24)
+    tabs, w = [M.rope_table(n, r) for n, r in ((21, 16), (10, 24), (10, 24))], torch.rand(64, generator=gen, device="cuda")
+    x, d = rnd(rows, 256), rnd(rows, 256)
+    want, got = M.qk_norm_rope(x, w, w, tabs, qk), far(none.expand(rows, 256), 1024)
+    M.qk_norm_rope(far(x, 0), w, w, tabs, qk, out=got)
+    assert torch.equal(got, want)
+    want = M.qk_norm_rope_backward(x, w, w, tabs, d, qk)
+    grads = M.qk_norm_rope_backward(far(x, 0), w, w, tabs, far(d, 512), qk, dqkv=got)
+    assert all(torch.equal(grads[k], want[k]) for k in want)
+    gs = M.GatedScanConfig(B=2, T=21, H=10, W=10, D=256, order=3, reverse=True)
+    g, st, st2 = rnd(rows, 256), M.gated_scan_states(gs), M.gated_scan_states(gs)
+    y, hl = M.gated_scan(x, g, gs, states=st)
+    yf, hf = M.gated_scan(far(x, 0), far(g, 512), gs, y=got, states=st2)
+    assert torch.equal(yf, y) and torch.equal(hf, hl) and torch.equal(st, st2)
+    want = M.gated_scan_backward(x, g, st, d, gs)
+    dx, dg = far(none.expand(rows, 256), 2048), far(none.expand(rows, 256), 4096)
+    grads = M.gated_scan_backward(big[:, :256], big[:, 512:768], st, far(d, 1024), gs, dx=dx, dg=dg)
+    assert all(torch.equal(grads[k], want[k]) for k in want)
+    wide = torch.empty((rows, ld), dtype=torch.int8, device="cuda")
+    q, s = M.quantize_rows(x)
+    qf, sf = M.quantize_rows(big[:, :256], q=wide[:, 64:320])
+    assert torch.equal(qf, q) and torch.equal(sf, s)
+    W, sw = M.quantize_rows(rnd(300, 256))
+    want = M.project_int8(q, s, W, sw)
+    assert torch.equal(M.project_int8(qf, s, W, sw, out=big[:, 8192:8192 + 300]), want)
+    assert torch.equal(M.project_int8(qf[-3:], s[-3:], W, sw, out=big[-3:, 8192:8192 + 300]), want[-3:])
+    # the weights' rows as far apart
+    Wf = wide[:, 512:768]
+    Wf.copy_(q)
+    assert torch.equal(M.project_int8(q[:64], s[:64], Wf, s), M.project_int8(q[:64], s[:64], q, s))
+    assert torch.equal(M.project_int8(q[:2], s[:2], Wf, s), M.project_int8(q[:2], s[:2], q, s))
